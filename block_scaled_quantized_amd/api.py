@@ -14,11 +14,15 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmxgemm.so")
 
 MX_E4M3, MX_E5M2, MX_E2M3, MX_E3M2, MX_E2M1, MX_E8M0, MX_F16, MX_INT8, MX_INT4 = 0, 1, 2, 3, 4, 8, 16, 32, 33
+MX_BF16, MX_F32 = 17, 18  # rotary positions and the key-value cache only
 MXGEMM_RELU = 1  # mxgemm_create flag: C = max(A*B, 0) in the epilogue
 MXGEMM_QUANT_A = 2  # mxgemm_create flag: A is binary16, quantised to E4M3 inside the GEMM
 MX_OK, MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT, MX_ERR_ARCH, MX_ERR_LAUNCH, MX_ERR_NOMEM = \
     0, -1, -2, -3, -4, -5, -6, -7
 MX_ERR_SCRATCH = -8
+MXROPE_HALF, MXROPE_PAIRS = 0, 1  # which elements a rotation pairs
+MXROPE_PLAIN, MXROPE_LINEAR, MXROPE_NTK, MXROPE_BANDS, MXROPE_YARN = range(5)  # frequency rules
+MXKV_HEADS_FIRST, MXKV_SLOTS_FIRST = 0, 1  # order of a page's elements
 MXMATVEC_SCRATCH_BYTES = 17 << 20  # static scratch of mxmatvec_run_noalloc, per GPU
 
 if not os.path.exists(LIB_PATH):
@@ -26,6 +30,30 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i, _u, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_int64
+
+_pi = ctypes.POINTER(_i)
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _vp), ("heads", _i), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", _i), ("layout", _i), ("freq", _vp), ("factor", ctypes.c_float)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("fmt", _i), ("order", _i), ("pages", _i), ("page_size", _i), ("heads", _i), ("dim", _i),
+                ("page_stride", _i64), ("k", _vp), ("v", _vp), ("ks", _vp), ("vs", _vp)]
+
+
+class _Table(ctypes.Structure):
+    _fields_ = [("pages", _vp), ("seqs", _i), ("cols", _i)]
+
+
+class _AttnOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", _i)]
+
 
 EXPORTS = {
     "mx_strerror": (ctypes.c_char_p, [_i]),
@@ -39,6 +67,21 @@ EXPORTS = {
     "mxmatvec_run_noalloc": (_i, [_i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp]),
     "mx_pack_run": (_i, [_i, _vp, _i, _i, _vp, _vp, _vp]),
     "mx_unpack_run": (_i, [_i, _vp, _vp, _i, _i, _vp, _vp]),
+    "mxrope_freqs_host": (_i, [_i, ctypes.c_double, _i, _vp, _vp, _vp]),
+    "mxrope_run": (_i, [_i, _vp, _i, _i, _vp, _vp, _vp, _i, _vp]),
+    "mxkv_append_run": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mxattn_decode_run": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
+    "mxattn_decode_workspace_size": (ctypes.c_size_t, [_vp, _i, _i, _i, _i]),
+    "mxkv_copy_run": (_i, [_vp, _i, _vp, _i, _vp]),
+    "mxkv_pool_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i]),
+    "mxkv_pool_destroy": (_i, [_vp]),
+    "mxkv_pool_resize": (_i, [_vp, _i, _i, _vp, _pi]),
+    "mxkv_pool_fork": (_i, [_vp, _i, _i]),
+    "mxkv_pool_reorder": (_i, [_vp, _vp]),
+    "mxkv_pool_compact": (_i, [_vp, _vp, _i, _pi]),
+    "mxkv_pool_table": (_vp, [_vp]),
+    "mxkv_pool_lengths": (_vp, [_vp]),
+    "mxkv_pool_used": (_i, [_vp]),
     "mx_pack_host": (_i, [_i, _vp, _i64, _i64, _vp, _vp]),
     "mx_unpack_host": (_i, [_i, _vp, _vp, _i64, _i64, _vp]),
     "mx_encode_host": (ctypes.c_uint8, [_i, ctypes.c_float]),
@@ -189,3 +232,185 @@ def mx_shapes(fmt: int, rows: int, K: int):
 def int_shapes(fw: int, K: int, N: int):
     """(codes shape, scales shape) of an int8/int4 weight W[K][N]."""
     return ((K, N // 2) if fw == MX_INT4 else (K, N)), (K // 32, N)
+
+
+# ---- the decode step's cache: rotary positions, append, attention, pages ------------------------
+
+class Rope:
+    """An mxrope: freq is a device tensor of rot_dim / 2 doubles, which is kept alive here."""
+
+    def __init__(self, rot_dim: int, freq, layout: int = MXROPE_HALF, factor: float = 1.0):
+        self.freq = freq
+        self.c = _Rope(rot_dim, layout, _ptr(freq), factor)
+        self.ref = ctypes.addressof(self.c)
+
+
+def mxrope_freqs_host(rot_dim: int, base: float, rule: int = MXROPE_PLAIN, params=()):
+    """(list of rot_dim / 2 angles per position, factor of cos and sin) of a frequency rule."""
+    freq, factor = (ctypes.c_double * max(1, rot_dim // 2))(), ctypes.c_float()
+    par = (ctypes.c_double * 4)(*params) if len(params) else None
+    _check(_lib.mxrope_freqs_host(rot_dim, base, rule, par, freq, ctypes.addressof(factor)), "mxrope_freqs_host")
+    return list(freq), factor.value
+
+
+def _heads(t) -> _Heads:
+    """A [tokens][heads][dim] tensor; dim must be contiguous."""
+    tokens, heads, dim = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and dim > 1:
+        raise MXError(MX_ERR_SHAPE, "mx_heads")
+    return _Heads(t.data_ptr(), heads, st, sh)
+
+
+def mxrope_run(f: int, rope: Rope, x, out, positions, inverse: bool = False, stream=None) -> None:
+    """x, out: [tokens][heads][dim] (out may be x); positions: int32 [tokens]."""
+    a, b = _heads(x), _heads(out)
+    if x.shape != out.shape:
+        raise MXError(MX_ERR_SHAPE, "mxrope_run")
+    _check(_lib.mxrope_run(f, rope.ref, x.shape[0], x.shape[2], ctypes.addressof(a), ctypes.addressof(b),
+                           _ints(positions, "mxrope_run", (x.shape[0],)), int(inverse), _stream(stream)), "mxrope_run")
+
+
+def _ints(t, where: str, shape):
+    """Address of a dense int32 tensor of this shape; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != _int32() or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise MXError(MX_ERR_SHAPE, where)
+    return t.data_ptr()
+
+
+def _int32():
+    import torch
+    return torch.int32
+
+
+class KVCache:
+    """An mxkv_cache over torch tensors, which are kept alive here: k and v are
+    [pages][heads][page_size][dim] (MXKV_HEADS_FIRST) or [pages][page_size][heads][dim]
+    (MXKV_SLOTS_FIRST), dense within a page; for MX_E4M3 bytes, with the scales ks, vs
+    [pages][..][..][dim / 32]."""
+
+    def __init__(self, fmt: int, k, v, ks=None, vs=None, order: int = MXKV_HEADS_FIRST):
+        pages, a, b, dim = k.shape
+        stride = k.stride(0) if pages > 1 else a * b * dim
+        for t, d, unit in ((k, dim, 1), (v, dim, 1), (ks, dim // 32, 32), (vs, dim // 32, 32)):
+            if t is None:
+                continue
+            if tuple(t.shape) != (pages, a, b, d) or not t[0].is_contiguous() or (pages > 1 and t.stride(0) * unit != stride):
+                raise MXError(MX_ERR_SHAPE, "KVCache")
+        heads, page_size = (a, b) if order == MXKV_HEADS_FIRST else (b, a)
+        self.tensors = (k, v, ks, vs)
+        self.c = _Cache(fmt, order, pages, page_size, heads, dim, stride, _ptr(k), _ptr(v), _ptr(ks), _ptr(vs))
+        self.ref = ctypes.addressof(self.c)
+
+
+def kv_layers(caches):
+    """The layers' caches as the array that mxkv_copy_run takes, for callers that keep it."""
+    arr = (_Cache * max(1, len(caches)))(*(x.c for x in caches))
+    arr.count, arr.caches = len(caches), list(caches)
+    return arr
+
+
+def _table(t, where: str) -> _Table:
+    seqs, cols = t.shape
+    return _Table(_ints(t, where, t.shape), seqs, cols)
+
+
+def mxkv_append_run(cache: KVCache, f: int, k, v, positions, table, seq=None, rope: Rope | None = None, q=None, q_out=None,
+                    stream=None) -> None:
+    """k, v: [tokens][heads][dim]; positions, seq: int32 [tokens]; table: int32 [seqs][cols]; q, q_out:
+    [tokens][q heads][dim], turned in the same launch."""
+    where, n, dim = "mxkv_append_run", k.shape[0], cache.c.dim
+    for t in (k, v, q, q_out):
+        if t is not None and (t.shape[0] != n or t.shape[2] != dim):
+            raise MXError(MX_ERR_SHAPE, where)
+    hk, hv, tab = _heads(k), _heads(v), _table(table, where)
+    hq, ho = (None if t is None else _heads(t) for t in (q, q_out))
+    _check(_lib.mxkv_append_run(cache.ref, f, n, ctypes.addressof(hk), ctypes.addressof(hv), _ints(positions, where, (n,)),
+                                _ints(seq, where, (n,)), ctypes.addressof(tab), rope.ref if rope else None,
+                                ctypes.addressof(hq) if hq else None, ctypes.addressof(ho) if ho else None,
+                                _stream(stream)), where)
+
+
+def mxattn_decode_workspace_size(cache: KVCache, seqs: int, q_heads: int, max_len: int, window: int = 0) -> int:
+    return int(_lib.mxattn_decode_workspace_size(cache.ref, seqs, q_heads, max_len, window))
+
+
+def mxattn_decode_run(cache: KVCache, f: int, q, out, table, lengths, max_len: int, scale: float, lse=None, starts=None,
+                      window: int = 0, softcap: float = 0.0, workspace=None, workspace_bytes=None, stream=None) -> None:
+    """q, out: [seqs][q heads][dim]; table: int32 [seqs][cols]; lengths, starts: int32 [seqs]; lse: fp32
+    [seqs][q heads]; workspace: a zero-filled device buffer (a tensor's own size when workspace_bytes is omitted)."""
+    where, n = "mxattn_decode_run", q.shape[0]
+    if q.shape != out.shape or q.shape[2] != cache.c.dim or table.shape[0] != n or \
+            (lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous())):
+        raise MXError(MX_ERR_SHAPE, where)
+    if workspace is not None and workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    hq, ho, tab, opts = _heads(q), _heads(out), _table(table, where), _AttnOpts(scale, softcap, window)
+    _check(_lib.mxattn_decode_run(cache.ref, f, ctypes.addressof(hq), ctypes.addressof(ho), _ptr(lse), ctypes.addressof(tab),
+                                  _ints(lengths, where, (n,)), _ints(starts, where, (n,)), max_len, ctypes.addressof(opts),
+                                  _ptr(workspace), int(workspace_bytes or 0), _stream(stream)), where)
+
+
+def mxkv_copy_run(caches, pairs, stream=None) -> None:
+    """caches: a list of KVCache, or kv_layers of it; pairs: int32 [n][2] of (source, destination) pages."""
+    arr = caches if isinstance(caches, ctypes.Array) else kv_layers(caches)
+    _check(_lib.mxkv_copy_run(ctypes.addressof(arr), arr.count, _ints(pairs, "mxkv_copy_run", (pairs.shape[0], 2)),
+                              pairs.shape[0], _stream(stream)), "mxkv_copy_run")
+
+
+class KVPool:
+    """Owns an mxkv_pool. Page pairs come back as lists of (source, destination) for mxkv_copy_run."""
+
+    def __init__(self, pages: int, page_size: int, seqs: int, cols: int):
+        h = _vp()
+        self.handle = None
+        _check(_lib.mxkv_pool_create(ctypes.byref(h), pages, page_size, seqs, cols), "mxkv_pool_create")
+        self.handle, self.pages, self.seqs, self.cols = h.value, pages, seqs, cols
+
+    def close(self):
+        if self.handle:
+            _lib.mxkv_pool_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def resize(self, seq: int, tokens: int):
+        pair, n = (ctypes.c_int32 * 2)(), _i()
+        _check(_lib.mxkv_pool_resize(self.handle, seq, tokens, pair, ctypes.byref(n)), "mxkv_pool_resize")
+        return [(pair[0], pair[1])] if n.value else []
+
+    def fork(self, src: int, dst: int) -> None:
+        _check(_lib.mxkv_pool_fork(self.handle, src, dst), "mxkv_pool_fork")
+
+    def reorder(self, source) -> None:
+        if len(source) != self.seqs:
+            raise MXError(MX_ERR_SHAPE, "mxkv_pool_reorder")
+        _check(_lib.mxkv_pool_reorder(self.handle, (ctypes.c_int32 * self.seqs)(*source)), "mxkv_pool_reorder")
+
+    def compact(self, max_pairs: int | None = None):
+        most = self.pages if max_pairs is None else max_pairs
+        pairs, n = (ctypes.c_int32 * max(1, 2 * most))(), _i()
+        _check(_lib.mxkv_pool_compact(self.handle, pairs, most, ctypes.byref(n)), "mxkv_pool_compact")
+        return [(pairs[2 * i], pairs[2 * i + 1]) for i in range(n.value)]
+
+    def _host(self, name, shape):
+        import numpy as np
+        at = getattr(_lib, name)(self.handle)
+        return np.ctypeslib.as_array(ctypes.cast(at, ctypes.POINTER(ctypes.c_int32)), shape).copy()
+
+    def table(self):
+        """numpy int32 [seqs][cols], -1 where a sequence has no page."""
+        return self._host("mxkv_pool_table", (self.seqs, self.cols))
+
+    def lengths(self):
+        return self._host("mxkv_pool_lengths", (self.seqs,))
+
+    @property
+    def used(self) -> int:
+        return _lib.mxkv_pool_used(self.handle)

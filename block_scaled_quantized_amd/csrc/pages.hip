@@ -1,0 +1,118 @@
+// pages.hip -- copies of whole pages of a paged key-value cache, over all layers in one launch.
+//
+// A page's elements lie together in either order, so a copy is a gather of contiguous pieces: the pairs'
+// bytes of a plane are numbered through, each thread takes four 16-byte words a workgroup's width apart
+// and finds its pair by a division by the page's words. Bound by memory: each byte is read and
+// written once.
+#include "kvcache.h"
+
+using namespace mx;
+
+namespace {
+
+constexpr int kThreads = 256, kWords = 4, kBlockWords = kThreads * kWords;
+constexpr int kLayers = 32;  // layers of one launch (their addresses are kernel arguments)
+
+struct Planes {
+  uint8_t* p[kLayers][4];  // k, v, ks, vs
+};
+
+// One kind of plane: `words` words of a page that is copied, one page every `stride` words.
+struct Shape {
+  int64_t stride;
+  int words, blocks;  // blocks: workgroups over all pairs
+  FastDiv div;
+};
+
+template <typename W>
+MX_DEV void copy_words(W* base, const Shape& s, const int32_t* __restrict__ pairs, int n_pairs, int pages, int block) {
+  // block's first word, as (pair, word of its page); the words after it are found from there in 32 bits
+  const int64_t first = (int64_t)block * kBlockWords;
+  const int pair0 = (int)(first / s.words), word0 = (int)(first - (int64_t)pair0 * s.words);
+  W v[kWords];
+  W* to[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; i++) {
+    const uint32_t w = (uint32_t)(word0 + i * kThreads + (int)threadIdx.x);
+    const int skip = (int)s.div.div(w), pair = pair0 + skip;
+    to[i] = nullptr;
+    if (pair >= n_pairs) continue;
+    const int src = pairs[2 * pair], dst = pairs[2 * pair + 1];
+    if (src < 0 || src >= pages || dst < 0 || dst >= pages || src == dst) continue;
+    const int64_t at = w - (uint32_t)skip * (uint32_t)s.words;
+    v[i] = base[src * s.stride + at];
+    to[i] = base + dst * s.stride + at;
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; i++)
+    if (to[i]) *to[i] = v[i];
+}
+
+__global__ __launch_bounds__(kThreads) void copy_kernel(Planes planes, Shape data, Shape scale, int scale_bytes,
+                                                        const int32_t* __restrict__ pairs, int n_pairs, int pages) {
+  // x: workgroups of the data plane, then of the scale plane; y: layer; z: keys or values
+  const int layer = blockIdx.y, kv = blockIdx.z;
+  int block = blockIdx.x;
+  if (block < data.blocks) {
+    copy_words((u32x4*)planes.p[layer][kv], data, pairs, n_pairs, pages, block);
+    return;
+  }
+  block -= data.blocks;
+  uint8_t* s = planes.p[layer][2 + kv];
+  if (scale_bytes == 16) copy_words((u32x4*)s, scale, pairs, n_pairs, pages, block);
+  else if (scale_bytes == 4) copy_words((uint32_t*)s, scale, pairs, n_pairs, pages, block);
+  else copy_words(s, scale, pairs, n_pairs, pages, block);
+}
+
+// False where the numbers do not fit the kernel's 32-bit words of a page.
+bool shape_of(int64_t page_bytes, int64_t stride_bytes, int word, int n_pairs, Shape& s, int64_t& blocks) {
+  if (page_bytes / word >= (int64_t)1 << 30) return false;
+  s.words = (int)(page_bytes / word);
+  s.stride = stride_bytes / word;
+  s.div = FastDiv((uint32_t)s.words);
+  blocks = ceil_div((int64_t)s.words * n_pairs, (int64_t)kBlockWords);
+  s.blocks = (int)blocks;
+  return blocks < 1 << 23;
+}
+
+}  // namespace
+
+extern "C" int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32_t* pairs, int n_pairs, void* stream) {
+  if (n_layers < 0 || n_layers > MX_MAX_DIM || n_pairs < 0 || n_pairs > MX_MAX_DIM) return MX_ERR_SHAPE;
+  if (n_layers > 0 && !layers) return MX_ERR_NULL;
+  for (int i = 0; i < n_layers; i++) {
+    const mxkv_cache &c = layers[i], &z = layers[0];
+    if (int s = check_cache(&c)) return s;
+    if (c.fmt != z.fmt || c.order != z.order || c.pages != z.pages || c.page_size != z.page_size || c.heads != z.heads ||
+        c.dim != z.dim || c.page_stride != z.page_stride)
+      return MX_ERR_SHAPE;
+  }
+  if (n_layers == 0 || n_pairs == 0) return MX_OK;
+  if (!pairs) return MX_ERR_NULL;
+  const mxkv_cache& c = layers[0];
+  const bool mx8 = c.fmt == MX_E4M3;
+  const int bytes = mx8 ? 1 : 2;
+  const int64_t elems = (int64_t)c.heads * c.page_size * c.dim;
+  Shape data = {}, scale = {};
+  int64_t blocks = 0, scale_blocks = 0;
+  if (!shape_of(elems * bytes, c.page_stride * bytes, 16, n_pairs, data, blocks)) return MX_ERR_SHAPE;
+  int word = 16;  // a page's scales need not be whole 16-byte words
+  if (mx8) {
+    while (word > 1 && ((elems / 32) % word || (c.page_stride / 32) % word)) word /= 4;
+    if (!shape_of(elems / 32, c.page_stride / 32, word, n_pairs, scale, scale_blocks)) return MX_ERR_SHAPE;
+  }
+  if (int s = check_arch()) return s;
+  const hipStream_t st = as_stream(stream);
+  for (int first = 0; first < n_layers; first += kLayers) {
+    const int n = n_layers - first < kLayers ? n_layers - first : kLayers;
+    Planes p = {};
+    for (int i = 0; i < n; i++) {
+      const mxkv_cache& l = layers[first + i];
+      p.p[i][0] = (uint8_t*)l.k, p.p[i][1] = (uint8_t*)l.v, p.p[i][2] = (uint8_t*)l.ks, p.p[i][3] = (uint8_t*)l.vs;
+    }
+    hipLaunchKernelGGL(copy_kernel, dim3((unsigned)(blocks + scale_blocks), (unsigned)n, 2), dim3(kThreads), 0, st, p, data, scale,
+                       word, pairs, n_pairs, c.pages);
+    if (int s = launch_status()) return s;
+  }
+  return sync_check(MX_OK, st);
+}

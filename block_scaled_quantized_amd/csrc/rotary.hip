@@ -1,0 +1,451 @@
+// rotary.hip -- rotary positions and the append to a paged key-value cache.
+//
+// Rotation: pair (a, b) of token t turns by w = pos[t] f[i]: (a cos w - b sin w, b cos w + a sin w).
+// Both kernels move each element once and are bound by memory (by latency for few tokens), so the
+// work per element is kept small: a workgroup takes a few tokens and a run of their heads, computes
+// the tokens' cosines and sines once into LDS, one (token, pair) per thread, while its first rows
+// are on their way, and every head reads them from there. The angle is reduced in 64 bits:
+// pos * f / 2 pi loses about 2^-52 of its value (2^20 positions: 2^-32 turns), where 32 bits would
+// lose the phase of far positions altogether; after the reduction to half a turn an fp32 sine and
+// cosine are exact to 2 ulp.
+#include <cmath>
+
+#include "kvcache.h"
+#include "quant_rules.h"
+
+using namespace mx;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;      // rows that a thread loads before it uses the first
+constexpr int kMaxTrig = 512;  // (token, pair) angles of a workgroup
+constexpr int kStage = 8192;   // 16-bit elements of rotated keys that a workgroup stages
+
+template <typename T>
+struct Unit {  // 16 bytes of elements
+  static constexpr int N = 16 / sizeof(T);
+  T e[N];
+};
+
+MX_DEV float to_f32(_Float16 x) { return (float)x; }
+MX_DEV float to_f32(__bf16 x) { return (float)x; }
+MX_DEV float to_f32(float x) { return x; }
+
+struct Rotation {
+  const double* freq;
+  int half;
+  float factor, sign;
+};
+
+// cos and sin of `tokens` x half angles from pos[t0] into trig[token * half + pair].
+MX_DEV void fill_trig(const Rotation& r, const int32_t* __restrict__ pos, int t0, int tokens, float2* trig) {
+  for (int i = threadIdx.x; i < tokens * r.half; i += kThreads) {
+    const int t = i / r.half;
+    double w = (double)pos[t0 + t] * r.freq[i - t * r.half] * 0.15915494309189533577;  // in turns
+    w -= __builtin_rint(w);
+    float s, c;
+    sincospif((float)(w + w), &s, &c);
+    trig[i] = make_float2(c * r.factor, s * r.factor * r.sign);
+  }
+}
+
+// How a head's dim elements are dealt to threads: `pairs` items that rotate, then `tail` items of
+// elements that are copied. VEC: an item moves whole 16-byte units (HALF: one of each half's, PAIRS:
+// one); else one pair or one element.
+struct Split {
+  int pairs, items;
+};
+
+// A workgroup's rows: tokens t0 .. t0 + tokens - 1 times heads h0 .. h0 + heads - 1. store(token, head,
+// element, values, count) takes a unit or single elements. COPY_TAIL: whether copied elements need a store.
+template <typename T, bool PAIRS, bool VEC, typename Store>
+MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, int t0, int tokens, const T* __restrict__ x,
+                        int64_t xt, int64_t xh, int h0, int heads, Split sp, bool copy_tail, float2* trig, Store store) {
+  constexpr int U = Unit<T>::N;
+  const int per = kThreads / sp.items;  // rows of one pass
+  const int item = threadIdx.x % sp.items, r0 = threadIdx.x / sp.items;
+  const bool turns = item < sp.pairs, mine = r0 < per && (turns || copy_tail);
+  const int rows = tokens * heads, half = rot.half;
+  // first element, and the second half's for HALF
+  const int a = VEC ? (turns ? U * item : 2 * half + U * (item - sp.pairs))
+                    : (turns ? (PAIRS ? 2 * item : item) : 2 * half + item - sp.pairs);
+  bool ready = false;
+  for (int base = r0; base - r0 < rows; base += per * kBatch) {  // the same number of turns for every thread
+    Unit<T> lo[kBatch], hi[kBatch];
+    int tok[kBatch], head[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      const int row = base + u * per;
+      tok[u] = row / heads;
+      head[u] = row - tok[u] * heads;
+      if (mine && row < rows) {
+        const T* p = x + (int64_t)(t0 + tok[u]) * xt + (int64_t)(h0 + head[u]) * xh + a;
+        if constexpr (VEC) {
+          lo[u] = *reinterpret_cast<const Unit<T>*>(p);
+          if (!PAIRS && turns) hi[u] = *reinterpret_cast<const Unit<T>*>(p + half);
+        } else {
+          lo[u].e[0] = p[0];
+          if (turns) hi[u].e[0] = p[PAIRS ? 1 : half];
+        }
+      }
+    }
+    if (!ready) {
+      fill_trig(rot, pos, t0, tokens, trig);
+      __syncthreads();
+      ready = true;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      if (!mine || base + u * per >= rows) continue;
+      if (turns) {
+        const float2* cs = trig + tok[u] * half + (VEC ? (PAIRS ? item * (U / 2) : item * U) : item);
+        if constexpr (VEC && PAIRS) {
+#pragma unroll
+          for (int i = 0; i < U / 2; i++) {
+            const float p = to_f32(lo[u].e[2 * i]), q = to_f32(lo[u].e[2 * i + 1]);
+            const float2 w = cs[i];
+            lo[u].e[2 * i] = (T)(p * w.x - q * w.y);
+            lo[u].e[2 * i + 1] = (T)(q * w.x + p * w.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < (VEC ? U : 1); i++) {
+            const float p = to_f32(lo[u].e[i]), q = to_f32(hi[u].e[i]);
+            const float2 w = cs[i];
+            lo[u].e[i] = (T)(p * w.x - q * w.y);
+            hi[u].e[i] = (T)(q * w.x + p * w.y);
+          }
+        }
+      }
+      store(tok[u], head[u], a, lo[u]);
+      if (turns && !(VEC && PAIRS)) store(tok[u], head[u], a + (PAIRS ? 1 : half), hi[u]);
+    }
+  }
+}
+
+template <typename T, bool VEC>
+MX_DEV void put(T* p, const Unit<T>& v) {
+  if constexpr (VEC) *reinterpret_cast<Unit<T>*>(p) = v;
+  else p[0] = v.e[0];
+}
+
+struct RopeArgs {
+  Rotation rot;
+  const int32_t* pos;
+  const void* x;
+  void* out;
+  int64_t xt, xh, ot, oh;
+  int tokens, heads, tile_t, tile_h, groups;  // groups: runs of tile_h heads
+  Split split;
+};
+
+template <typename T, bool PAIRS, bool VEC>
+MX_DEV void rope_block(const RopeArgs& a, int block, float2* trig) {
+  const int g = block % a.groups, t0 = (block / a.groups) * a.tile_t, h0 = g * a.tile_h;
+  T* out = (T*)a.out;
+  rotate_rows<T, PAIRS, VEC>(a.rot, a.pos, t0, min(a.tile_t, a.tokens - t0), (const T*)a.x, a.xt, a.xh, h0,
+                             min(a.tile_h, a.heads - h0), a.split, a.x != a.out, trig,
+                             [&](int t, int h, int e, const Unit<T>& v) {
+                               put<T, VEC>(out + (int64_t)(t0 + t) * a.ot + (int64_t)(h0 + h) * a.oh + e, v);
+                             });
+}
+
+template <typename T, bool PAIRS, bool VEC>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
+  __shared__ float2 trig[kMaxTrig];
+  rope_block<T, PAIRS, VEC>(a, blockIdx.x, trig);
+}
+
+// ---- append ---------------------------------------------------------------------------------
+
+struct AppendArgs {
+  RopeArgs q;       // the queries' blocks come first ...
+  RopeArgs k;       // ... then the keys' ... (out unused)
+  const void* v;    // ... then the values'
+  int64_t vt, vh;
+  int q_blocks, k_blocks;
+  bool turn;  // keys are rotated
+  const int32_t *seq, *table;
+  int seqs, cols, pages, page_size, dim;
+  int64_t page_stride, head_stride, slot_stride;
+  uint8_t *kc, *vc, *ks, *vs;
+  FastDiv page_div;
+};
+
+// Element offset of each token's slot (head 0) in the cache, -1 where it has none.
+MX_DEV void fill_slots(const AppendArgs& a, int t0, int tokens, int64_t* slot) {
+  for (int t = threadIdx.x; t < tokens; t += kThreads) {
+    const int p = a.k.pos[t0 + t], s = a.seq ? a.seq[t0 + t] : t0 + t;
+    int64_t at = -1;
+    if (p >= 0 && s >= 0 && s < a.seqs) {
+      const int c = (int)a.page_div.div((uint32_t)p);
+      if (c < a.cols) {
+        const int page = a.table[(int64_t)s * a.cols + c];
+        if (page >= 0 && page < a.pages) at = page * a.page_stride + (p - c * a.page_size) * a.slot_stride;
+      }
+    }
+    slot[t] = at;
+  }
+}
+
+// Eight elements of a row to their place `at` in a plane (-1: nowhere).
+template <typename T>
+MX_DEV void write_unit(const Unit<T>& v, bool mx8, uint8_t* codes, uint8_t* scales, int64_t at) {
+  if (!mx8) {
+    if (at >= 0) *reinterpret_cast<Unit<T>*>(codes + 2 * at) = v;
+    return;
+  }
+  // Four neighbouring lanes hold a block of 32: they agree on its scale, and each writes its 8 codes.
+  float x[8];
+  uint32_t amax = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    x[i] = to_f32(v.e[i]);
+    amax = max(amax, fbits(x[i]) & 0x7FFFFFFFu);  // NaN and Inf have the largest patterns
+  }
+  amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1));
+  amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
+  const bool nonfinite = amax >= 0x7F800000u;
+  int t;
+  const uint32_t E = mx_block_scale(amax, nonfinite, MX_E4M3, &t);
+  // gfx950's scaled conversion rounds as the rule does and writes NaN where it should saturate: those
+  // bytes become +-448 (the GPU pack's conversion).
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  const float scale = bitsf(E << 23);
+  u32x2 w;
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    s16x2 r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32((s16x2){0, 0}, x[4 * i], x[4 * i + 1], scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, x[4 * i + 2], x[4 * i + 3], scale, true);
+    uint32_t c = __builtin_bit_cast(uint32_t, r);
+    c ^= (((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+    w[i] = nonfinite ? 0u : c;
+  }
+  if (at < 0) return;
+  *reinterpret_cast<u32x2*>(codes + at) = w;
+  if (at % 32 == 0) scales[at / 32] = (uint8_t)E;
+}
+
+template <typename T, bool PAIRS, bool VEC>
+__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8) {
+  __shared__ float2 trig[kMaxTrig];
+  __shared__ T stage[kStage];
+  __shared__ int64_t slot[kMaxTrig];
+  int block = blockIdx.x;
+  if (block < a.q_blocks) {
+    rope_block<T, PAIRS, VEC>(a.q, block, trig);
+    return;
+  }
+  block -= a.q_blocks;
+  const bool key = block < a.k_blocks;
+  if (!key) block -= a.k_blocks;
+  const int g = block % a.k.groups, t0 = (block / a.k.groups) * a.k.tile_t, h0 = g * a.k.tile_h;
+  const int tokens = min(a.k.tile_t, a.k.tokens - t0), heads = min(a.k.tile_h, a.k.heads - h0);
+  fill_slots(a, t0, tokens, slot);
+  if (key && a.turn)
+    rotate_rows<T, PAIRS, VEC>(a.k.rot, a.k.pos, t0, tokens, (const T*)a.k.x, a.k.xt, a.k.xh, h0, heads, a.k.split, true, trig,
+                               [&](int t, int h, int e, const Unit<T>& v) {
+                                 put<T, VEC>(stage + (t * heads + h) * a.dim + e, v);
+                               });
+  __syncthreads();
+  // Rows go out in units of 8 elements; dim / 8 divides nothing in general, so threads past the last
+  // whole row of a pass idle (they still take part in the lane exchange).
+  const int units = a.dim / 8, per = kThreads / units, unit = threadIdx.x % units, r0 = threadIdx.x / units;
+  const T* x = key ? (const T*)a.k.x : (const T*)a.v;
+  const int64_t xt = key ? a.k.xt : a.vt, xh = key ? a.k.xh : a.vh;
+  uint8_t *codes = key ? a.kc : a.vc, *scales = key ? a.ks : a.vs;
+  for (int base = 0; base < tokens * heads; base += per) {
+    const int row = base + r0;
+    const bool mine = r0 < per && row < tokens * heads;
+    const int t = mine ? row / heads : 0, h = mine ? row - t * heads : 0;
+    Unit<T> v = {};
+    if (mine)
+      v = key && a.turn ? *reinterpret_cast<const Unit<T>*>(stage + row * a.dim + 8 * unit)
+                        : *reinterpret_cast<const Unit<T>*>(x + (int64_t)(t0 + t) * xt + (int64_t)(h0 + h) * xh + 8 * unit);
+    const int64_t s = mine ? slot[t] : -1;
+    write_unit<T>(v, mx8, codes, scales, s < 0 ? -1 : s + (h0 + h) * a.head_stride + 8 * unit);
+  }
+}
+
+// ---- host -----------------------------------------------------------------------------------
+
+bool vec_ok(int layout, int rot_dim, int unit) { return (layout == MXROPE_HALF ? rot_dim / 2 : rot_dim) % unit == 0; }
+
+Split split_of(int layout, int rot_dim, int dim, int unit, bool vec) {
+  Split s;
+  if (vec) {
+    s.pairs = layout == MXROPE_HALF ? rot_dim / 2 / unit : rot_dim / unit;
+    s.items = s.pairs + (dim - rot_dim) / unit;
+  } else {
+    s.pairs = rot_dim / 2;
+    s.items = s.pairs + dim - rot_dim;
+  }
+  return s;
+}
+
+// Tokens and heads of a workgroup. max_rows bounds tile_t * tile_h.
+void tile(RopeArgs& a, int max_rows) {
+  const int per = kThreads / a.split.items;  // rows of a pass
+  const int half = a.rot.half > 0 ? a.rot.half : 1;
+  a.tile_h = a.heads < max_rows ? a.heads : max_rows;
+  const int cap = max_rows < per * kBatch ? max_rows : per * kBatch;  // one batch of loads per thread
+  a.tile_t = 1;
+  while (2 * a.tile_t * a.tile_h <= cap && 2 * a.tile_t * half <= kMaxTrig && (a.tokens + a.tile_t - 1) / a.tile_t > 1024)
+    a.tile_t *= 2;
+  // few tokens: spread a token's heads over workgroups instead
+  while (a.tile_t == 1 && a.tile_h > per && (int64_t)a.tokens * ceil_div(a.heads, a.tile_h) < 512) a.tile_h = ceil_div(a.tile_h, 2);
+  a.groups = ceil_div(a.heads, a.tile_h);
+}
+
+int64_t blocks_of(const RopeArgs& a) { return (int64_t)ceil_div(a.tokens, a.tile_t) * a.groups; }
+
+int check_rope(const mxrope* r, int dim) {
+  if (!r || !r->freq) return MX_ERR_NULL;
+  if (r->layout != MXROPE_HALF && r->layout != MXROPE_PAIRS) return MX_ERR_FORMAT;
+  if (r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > dim) return MX_ERR_SHAPE;
+  return (reinterpret_cast<uintptr_t>(r->freq) & 7u) ? MX_ERR_ALIGN : MX_OK;
+}
+
+RopeArgs rope_args(const mxrope* r, int tokens, int dim, const mx_heads* x, const mx_heads* out, const int32_t* pos, int inverse,
+                   int unit, bool vec) {
+  RopeArgs a = {};
+  a.rot = {r ? r->freq : nullptr, r ? r->rot_dim / 2 : 0, r ? r->factor : 1.0f, inverse ? -1.0f : 1.0f};
+  a.pos = pos;
+  a.x = x->data, a.xt = x->token_stride, a.xh = x->head_stride;
+  if (out) a.out = out->data, a.ot = out->token_stride, a.oh = out->head_stride;
+  a.tokens = tokens, a.heads = x->heads;
+  a.split = split_of(r ? r->layout : MXROPE_HALF, r ? r->rot_dim : 0, dim, unit, vec);
+  return a;
+}
+
+template <typename T>
+void rope_launch(const RopeArgs& a, bool pairs, bool vec, dim3 grid, hipStream_t st) {
+  const dim3 block(kThreads);
+  if (pairs && vec) hipLaunchKernelGGL((rope_kernel<T, true, true>), grid, block, 0, st, a);
+  else if (pairs) hipLaunchKernelGGL((rope_kernel<T, true, false>), grid, block, 0, st, a);
+  else if (vec) hipLaunchKernelGGL((rope_kernel<T, false, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((rope_kernel<T, false, false>), grid, block, 0, st, a);
+}
+
+template <typename T>
+void append_launch(const AppendArgs& a, bool pairs, bool vec, bool mx8, dim3 grid, hipStream_t st) {
+  const dim3 block(kThreads);
+  if (pairs && vec) hipLaunchKernelGGL((append_kernel<T, true, true>), grid, block, 0, st, a, mx8);
+  else if (pairs) hipLaunchKernelGGL((append_kernel<T, true, false>), grid, block, 0, st, a, mx8);
+  else if (vec) hipLaunchKernelGGL((append_kernel<T, false, true>), grid, block, 0, st, a, mx8);
+  else hipLaunchKernelGGL((append_kernel<T, false, false>), grid, block, 0, st, a, mx8);
+}
+
+}  // namespace
+
+extern "C" int mxrope_freqs_host(int rot_dim, double base, int rule, const double* params, double* freq, float* factor) {
+  if (!freq || !factor) return MX_ERR_NULL;
+  if (rule < MXROPE_PLAIN || rule > MXROPE_YARN) return MX_ERR_FORMAT;
+  if (rule != MXROPE_PLAIN && !params) return MX_ERR_NULL;
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > kMaxHeadDim || !(base > 0) || !std::isfinite(base)) return MX_ERR_SHAPE;
+  const int count = rule == MXROPE_PLAIN ? 0 : rule <= MXROPE_NTK ? 1 : 4;
+  for (int i = 0; i < count; i++)
+    if (!std::isfinite(params[i]) || (i < 2 && !(params[i] > 0))) return MX_ERR_SHAPE;
+  if (rule == MXROPE_BANDS && !(params[3] > params[2])) return MX_ERR_SHAPE;
+  if (rule == MXROPE_YARN && !(base > 1 && params[2] > 0 && params[3] > 0)) return MX_ERR_SHAPE;
+  if (rule == MXROPE_NTK && rot_dim > 2) base *= std::pow(params[0], rot_dim / (rot_dim - 2.0));
+  const double turn = 2 * 3.14159265358979323846;
+  double lo = 0, hi = 0;
+  if (rule == MXROPE_YARN) {
+    const auto at = [&](double turns) { return rot_dim * std::log(params[1] / (turns * turn)) / (2 * std::log(base)); };
+    lo = std::fmax(std::floor(at(params[2])), 0.0);
+    hi = std::fmin(std::ceil(at(params[3])), rot_dim - 1.0);
+  }
+  for (int i = 0; i < rot_dim / 2; i++) {
+    const double f = std::pow(base, -2.0 * i / rot_dim);
+    double k;  // share of the frequency that is kept
+    switch (rule) {
+      case MXROPE_LINEAR: k = 0; break;
+      case MXROPE_BANDS: k = std::fmin(std::fmax((params[1] * f / turn - params[2]) / (params[3] - params[2]), 0.0), 1.0); break;
+      case MXROPE_YARN: k = 1 - std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0); break;
+      default: k = 1;
+    }
+    freq[i] = k == 1 ? f : (1 - k) * f / params[0] + k * f;
+  }
+  *factor = rule == MXROPE_YARN ? (float)(0.1 * std::log(params[0]) + 1.0) : 1.0f;
+  return MX_OK;
+}
+
+extern "C" int mxrope_run(int f, const mxrope* rope, int tokens, int dim, const mx_heads* x, const mx_heads* out,
+                          const int32_t* positions, int inverse, void* stream) {
+  if (f != MX_F16 && f != MX_BF16 && f != MX_F32) return MX_ERR_FORMAT;
+  if (!rope || !x || !out) return MX_ERR_NULL;
+  if (tokens < 0 || tokens > MX_MAX_DIM || !dim_ok(dim)) return MX_ERR_SHAPE;
+  if (int s = check_rope(rope, dim)) return s;
+  const int bytes = f == MX_F32 ? 4 : 2;
+  if (tokens == 0) return MX_OK;
+  if (!positions) return MX_ERR_NULL;
+  if (int s = check_heads(x, bytes)) return s;
+  if (int s = check_heads(out, bytes)) return s;
+  if (x->heads != out->heads) return MX_ERR_SHAPE;
+  if (x->data == out->data && (x->token_stride != out->token_stride || x->head_stride != out->head_stride)) return MX_ERR_SHAPE;
+  const bool pairs = rope->layout == MXROPE_PAIRS, vec = vec_ok(rope->layout, rope->rot_dim, 16 / bytes);
+  RopeArgs a = rope_args(rope, tokens, dim, x, out, positions, inverse, 16 / bytes, vec);
+  tile(a, 1 << 20);
+  if (int s = check_arch()) return s;
+  const hipStream_t st = as_stream(stream);
+  const dim3 grid((unsigned)blocks_of(a));  // at most tokens + 1024
+  if (f == MX_F16) rope_launch<_Float16>(a, pairs, vec, grid, st);
+  else if (f == MX_BF16) rope_launch<__bf16>(a, pairs, vec, grid, st);
+  else rope_launch<float>(a, pairs, vec, grid, st);
+  return sync_check(launch_status(), st);
+}
+
+extern "C" int mxkv_append_run(const mxkv_cache* cache, int f, int tokens, const mx_heads* k, const mx_heads* v,
+                               const int32_t* positions, const int32_t* seq, const mxkv_table* table, const mxrope* rope,
+                               const mx_heads* q, const mx_heads* q_out, void* stream) {
+  if (!cache || !k || !v || !table) return MX_ERR_NULL;
+  if (f != MX_F16 && f != MX_BF16) return MX_ERR_FORMAT;
+  if (int s = check_cache(cache)) return s;
+  const bool mx8 = cache->fmt == MX_E4M3;
+  if (!mx8 && cache->fmt != f) return MX_ERR_FORMAT;
+  if (tokens < 0 || tokens > MX_MAX_DIM) return MX_ERR_SHAPE;
+  if (int s = check_table(table)) return s;
+  if ((q == nullptr) != (q_out == nullptr) || (q && !rope)) return MX_ERR_NULL;
+  if (rope)
+    if (int s = check_rope(rope, cache->dim)) return s;
+  if (tokens == 0) return MX_OK;
+  if (!positions) return MX_ERR_NULL;
+  if (int s = check_heads(k, 2)) return s;
+  if (int s = check_heads(v, 2)) return s;
+  if (k->heads != cache->heads || v->heads != cache->heads) return MX_ERR_SHAPE;
+  if (q) {
+    if (int s = check_heads(q, 2)) return s;
+    if (int s = check_heads(q_out, 2)) return s;
+    if (q->heads != q_out->heads) return MX_ERR_SHAPE;
+    if (q->data == q_out->data && (q->token_stride != q_out->token_stride || q->head_stride != q_out->head_stride))
+      return MX_ERR_SHAPE;
+  }
+  const bool pairs = rope && rope->layout == MXROPE_PAIRS, vec = !rope || vec_ok(rope->layout, rope->rot_dim, 8);
+  AppendArgs a = {};
+  a.k = rope_args(rope, tokens, cache->dim, k, nullptr, positions, 0, 8, vec);
+  tile(a.k, kStage / cache->dim);
+  int64_t q_blocks = 0;
+  if (q) {
+    a.q = rope_args(rope, tokens, cache->dim, q, q_out, positions, 0, 8, vec);
+    tile(a.q, 1 << 20);
+    q_blocks = blocks_of(a.q);
+  }
+  const int64_t k_blocks = blocks_of(a.k);
+  if (q_blocks + 2 * k_blocks >= 1 << 24) return MX_ERR_SHAPE;
+  a.v = v->data, a.vt = v->token_stride, a.vh = v->head_stride;
+  a.q_blocks = (int)q_blocks, a.k_blocks = (int)k_blocks;
+  a.turn = rope != nullptr;
+  a.seq = seq, a.table = table->pages, a.seqs = table->seqs, a.cols = table->cols;
+  a.pages = cache->pages, a.page_size = cache->page_size, a.dim = cache->dim;
+  a.page_stride = cache->page_stride, a.head_stride = kv_head_stride(cache), a.slot_stride = slot_stride(cache);
+  a.kc = (uint8_t*)cache->k, a.vc = (uint8_t*)cache->v, a.ks = (uint8_t*)cache->ks, a.vs = (uint8_t*)cache->vs;
+  a.page_div = FastDiv((uint32_t)cache->page_size);
+  if (int s = check_arch()) return s;
+  const hipStream_t st = as_stream(stream);
+  const dim3 grid((unsigned)(q_blocks + 2 * k_blocks));
+  if (f == MX_F16) append_launch<_Float16>(a, pairs, vec, mx8, grid, st);
+  else append_launch<__bf16>(a, pairs, vec, mx8, grid, st);
+  return sync_check(launch_status(), st);
+}

@@ -1,6 +1,7 @@
 /*
  * mxgemm.h -- C ABI of libmxgemm.so: block-scaled (MX) quantized GEMM, fp16 GEMM, int8/int4
- * dequant matvec and the MX/int codecs, for AMD Instinct MI355X (gfx950).
+ * dequant matvec, the MX/int codecs, and the decode step's rotary positions, paged key-value cache
+ * and attention, for AMD Instinct MI355X (gfx950).
  *
  * Conventions shared by every entry point
  *  - Every function returns an mx_status; 0 is success. Arguments are validated before any work
@@ -29,6 +30,7 @@
  *  - Scales of MX operands: E8M0 bytes, value 2^(e-127), 0xFF = NaN; one scale per 32
  *    consecutive elements along K ("Scale planes: one MTLTensor = data + scales" and the
  *    auxiliary-plane blockFactors {32,1} of the WWDC26 session 330 summary).
+ *  - MX_BF16: bfloat16, and MX_F32: binary32 (rotary positions and the key-value cache only).
  *  - MX_F16: IEEE binary16. MX_INT8: two's-complement bytes. MX_INT4: two's-complement nibbles,
  *    packed two per byte along the C-order linear index, the even index in the low nibble
  *    ("TensorOps ... notes", section "VALIDATED ON M4 MAX", fact 5).
@@ -52,12 +54,12 @@ typedef enum {
   MX_ERR_ARCH = -5,    /* the current device is not gfx950, or no device is present */
   MX_ERR_LAUNCH = -6,  /* the HIP runtime reported an error when queueing a kernel (or, with
                           MX_SYNC_CHECK, when the stream ran it) */
-  MX_ERR_NOMEM = -7,   /* host allocation of a plan failed */
+  MX_ERR_NOMEM = -7,   /* host allocation of a plan failed, or a page pool has no page left */
   MX_ERR_SCRATCH = -8  /* mxmatvec_run_noalloc: the shape needs more than MXMATVEC_SCRATCH_BYTES */
 } mx_status;
 
 /* MX_E8M0 names the scale format; it is accepted only by mx_decode_host. */
-typedef enum { MX_E4M3 = 0, MX_E5M2 = 1, MX_E2M3 = 2, MX_E3M2 = 3, MX_E2M1 = 4, MX_E8M0 = 8, MX_F16 = 16, MX_INT8 = 32, MX_INT4 = 33 } mx_format;
+typedef enum { MX_E4M3 = 0, MX_E5M2 = 1, MX_E2M3 = 2, MX_E3M2 = 3, MX_E2M1 = 4, MX_E8M0 = 8, MX_F16 = 16, MX_BF16 = 17, MX_F32 = 18, MX_INT8 = 32, MX_INT4 = 33 } mx_format;
 
 /* Largest accepted dimension of any matrix (rows or columns). */
 #define MX_MAX_DIM (1 << 20)
@@ -285,6 +287,191 @@ int mx_unpack_host(int f, const void* codes, const void* scales, int64_t rows, i
  * MX_E8M0, MX_INT8 or MX_INT4 (low nibble); NaN for other f. */
 uint8_t mx_encode_host(int f, float v);
 float mx_decode_host(int f, uint8_t code);
+
+/* ------------------------------------------------------------------------------------------ */
+/* The decode step's cache: rotary positions, a paged key-value cache, attention over it.       */
+/* ------------------------------------------------------------------------------------------ */
+
+/* A tensor [tokens][heads][dim] with dim contiguous; strides in elements, each a multiple of 8 (of 4
+ * for MX_F32), so that every row is 16-byte aligned. */
+typedef struct {
+  void* data;
+  int heads;
+  int64_t token_stride, head_stride;
+} mx_heads;
+
+/* Which elements of a head form a rotated pair: i and i + rot_dim/2, or 2i and 2i + 1. */
+typedef enum { MXROPE_HALF = 0, MXROPE_PAIRS = 1 } mxrope_layout;
+
+/* A rotation: the first rot_dim elements of every head (even, 2 <= rot_dim <= dim); freq holds
+ * rot_dim/2 doubles on the device, pair i turning by freq[i] radians per position; cos and sin are
+ * multiplied by factor (1 for a plain rotation). */
+typedef struct {
+  int rot_dim, layout;
+  const double* freq;
+  float factor;
+} mxrope;
+
+/* Frequency rules of mxrope_freqs_host: with f_i = base^(-2i / rot_dim),
+ *  MXROPE_PLAIN   f_i;
+ *  MXROPE_LINEAR  f_i / params[0] (positions interpolated);
+ *  MXROPE_NTK     f_i with base * params[0]^(rot_dim / (rot_dim - 2)) (rot_dim = 2: the base as it is);
+ *  MXROPE_BANDS   params {s, trained length L, low, high}: blended by turns t_i = L f_i / 2 pi with
+ *                 k = clamp((t_i - low) / (high - low), 0, 1): (1 - k) f_i / s + k f_i;
+ *  MXROPE_YARN    params {s, L, fast, slow}: r_i = clamp((i - a) / max(c - a, 0.001), 0, 1) with a and c
+ *                 the pair indexes that make `fast` and `slow` turns over L, rounded down and up and
+ *                 cut to 0 and rot_dim - 1: r f_i / s + (1 - r) f_i, and factor 0.1 ln(s) + 1. */
+typedef enum { MXROPE_PLAIN = 0, MXROPE_LINEAR = 1, MXROPE_NTK = 2, MXROPE_BANDS = 3, MXROPE_YARN = 4 } mxrope_rule;
+
+/* mxrope_freqs_host -- freq[rot_dim/2] (host memory) and *factor of a frequency rule. params: the
+ * rule's parameters (NULL for MXROPE_PLAIN). MX_ERR_SHAPE: rot_dim odd, below 2 or above 256, or
+ * base, s, L or (high - low) not positive (base and fast, slow: above 1 and 0). Errors write
+ * nothing. */
+int mxrope_freqs_host(int rot_dim, double base, int rule, const double* params, double* freq, float* factor);
+
+/*
+ * mxrope_run -- out[t,h] = x[t,h] with each pair (a, b) of its first rot_dim elements turned by the
+ * angle w = positions[t] * freq[i]:  (a cos w - b sin w, b cos w + a sin w) * factor; the other
+ * elements are copied. inverse != 0 turns by -w: the gradient of the rotation with respect to x,
+ * applied to the output's gradient. f: MX_F16, MX_BF16 or MX_F32 (x and out). Angles are reduced
+ * in 64 bits (far positions keep their phase), the products are formed in fp32 and rounded once.
+ * x->heads == out->heads; 8 <= dim <= 256, dim % 8 == 0; 0 <= tokens <= MX_MAX_DIM (0: nothing is
+ * done), 1 <= heads <= 65536; positions: int32 [tokens], of any sign. out may be x itself (same data and strides);
+ * otherwise the two must not overlap, and no two rows of out may.
+ */
+int mxrope_run(int f, const mxrope* rope, int tokens, int dim, const mx_heads* x, const mx_heads* out,
+               const int32_t* positions, int inverse, void* stream);
+
+/* Order of a page's elements: [heads][page_size][dim] or [page_size][heads][dim]. */
+typedef enum { MXKV_HEADS_FIRST = 0, MXKV_SLOTS_FIRST = 1 } mxkv_order;
+
+/*
+ * A paged key-value cache (one layer's). k and v hold `pages` pages of page_size slots each, one
+ * page every page_stride elements, in `fmt`: MX_F16, MX_BF16, or MX_E4M3 codes with E8M0 scales per
+ * 32 elements of dim in ks and vs, where element e of k has its scale at ks[e / 32]. Keys and values
+ * may share one allocation (k at its start, v one page further, page_stride of two pages).
+ * Rules (MX_ERR_SHAPE): 8 <= dim <= 256 with dim % 8 == 0 (MX_E4M3: dim % 32 == 0);
+ * 1 <= heads <= 1024; 1 <= page_size <= MX_MAX_DIM; pages >= 1; pages * page_size < 2^31;
+ * page_stride >= heads * page_size * dim and a multiple of 8 (MX_E4M3: of 32).
+ */
+typedef struct {
+  int fmt, order, pages, page_size, heads, dim;
+  int64_t page_stride;
+  void *k, *v, *ks, *vs;
+} mxkv_cache;
+
+/* Page tables on the device: int32 [seqs][cols]; row s, column c is the page of sequence s's positions
+ * c * page_size .. c * page_size + page_size - 1. An entry outside 0 .. pages - 1 is no page: nothing
+ * is written to it, and attention leaves its positions out. */
+typedef struct {
+  const int32_t* pages;
+  int seqs, cols;
+} mxkv_table;
+
+/*
+ * mxkv_append_run -- write `tokens` new keys and values into the cache, in one launch with the
+ * rotation of the keys and of the step's queries. Token t belongs to sequence seq[t] (NULL: t) and
+ * goes to the slot of positions[t] in that sequence's table row. f: MX_F16 or MX_BF16 (k, v, q,
+ * q_out); the cache's format is f or MX_E4M3.
+ *  - rope != NULL: keys are turned as by mxrope_run (and rounded to f) before they are written.
+ *  - MX_E4M3: every 32 elements are quantised by the rule of mx_pack_run, with the same codes and scales.
+ *  - q, q_out != NULL (both or neither; rope needed): q_out = q turned, as by mxrope_run; q_out may be
+ *    q itself. A token without a slot still has its q turned.
+ *  - A token whose sequence, position or page is out of range is not written. Two tokens of one call
+ *    must not share a slot.
+ * tokens: 0 .. MX_MAX_DIM, and fewer than 2^24 workgroups. MX_ERR_SHAPE: head counts that disagree with the cache, bad strides.
+ */
+int mxkv_append_run(const mxkv_cache* cache, int f, int tokens, const mx_heads* k, const mx_heads* v,
+                    const int32_t* positions, const int32_t* seq, const mxkv_table* table, const mxrope* rope,
+                    const mx_heads* q, const mx_heads* q_out, void* stream);
+
+/* What mxattn_decode_run computes besides the plain softmax. scale: factor of q.k (usually
+ * dim^-1/2). softcap: c > 0 replaces a score s by c tanh(s / c); 0: off. window: w > 0 leaves only the
+ * last w positions; 0: off. */
+typedef struct {
+  float scale, softcap;
+  int window;
+} mxattn_opts;
+
+/*
+ * mxattn_decode_run -- attention of one new token per sequence over its paged cache:
+ *   s_j = scale * q[b,h] . k_j,  out[b,h] = sum_j e^{s_j} v_j / sum_j e^{s_j},  lse[b,h] = ln sum_j e^{s_j}
+ * over the positions j of sequence b with starts[b] <= j < lengths[b] (starts NULL: 0), within the
+ * window, whose page exists. Head h of q reads head h / (q->heads / cache->heads) of the cache.
+ *  - f: MX_F16 or MX_BF16 (q, out); the cache's format is f or MX_E4M3. q, out: [seqs][q heads][dim].
+ *  - A row with no position (an empty sequence, say) gives out = 0 and lse = -inf. lse, fp32
+ *    [seqs][q heads], may be NULL.
+ *  - Positions outside the range are never used, whatever their slots hold (NaN included). lengths
+ *    above max_len, or above cols * page_size, are taken as that bound; negative ones as 0.
+ *  - Scores, statistics and sums are fp32; the probabilities are rounded to 16 bits for the matrix
+ *    cores. E4M3 elements are scaled into f's format (exact in bfloat16; in binary16 where the value
+ *    is in its range, as every value that mxkv_append_run wrote from binary16 is).
+ * Workspace, as for mxmatvec_run: the sequences' lengths are split over workgroups, whose partial
+ * results and one counter per row of workgroups live in a caller-owned device buffer of
+ * mxattn_decode_workspace_size() bytes, zero-filled before its first use and left reusable by every
+ * call. Calls that may overlap in time need separate workspaces. Without one, or with too small a one, a
+ * sequence is not split (same results up to fp32 summation order; slow for long sequences). The
+ * partials are joined in a fixed order: results are deterministic.
+ * Rules (MX_ERR_SHAPE): q->heads a multiple of the cache's heads, out->heads == q->heads;
+ * seqs * q->heads < 2^24; 1 <= max_len < 2^30; scale finite, softcap and window not negative. table->seqs is the batch
+ * (0: nothing is done).
+ */
+int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, float* lse,
+                      const mxkv_table* table, const int32_t* lengths, const int32_t* starts, int max_len,
+                      const mxattn_opts* opts, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes mxattn_decode_run uses for these sizes (0: none needed, or invalid arguments); only
+ * the geometry of `cache` is read. */
+size_t mxattn_decode_workspace_size(const mxkv_cache* cache, int seqs, int q_heads, int max_len, int window);
+
+/*
+ * mxkv_copy_run -- copy whole pages (keys, values and scales) of n_layers caches of one geometry, which
+ * may be different allocations: page pairs[i][0] to page pairs[i][1] for every i < n_pairs, in every
+ * layer. pairs: int32 [n_pairs][2] on the device. Pairs run in no order: the destinations must be
+ * distinct, and none of them a source. Pairs with a page out of range, or of a page with itself, are
+ * ignored. layers: host array, read before the call returns. n_layers, n_pairs: 0 .. MX_MAX_DIM (0:
+ * nothing is done). MX_ERR_SHAPE also where the layers' geometry differs.
+ */
+int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32_t* pairs, int n_pairs, void* stream);
+
+/*
+ * mxkv_pool -- host bookkeeping of a cache's pages: which page belongs to which sequences, as tables
+ * for the calls above. Host only, queues no GPU work; not safe for concurrent calls on one pool. A new
+ * page is always the free one with the lowest number. Sequences may share pages (fork); a page is free
+ * when no sequence holds it. Functions that hand out page pairs expect the caller to queue
+ * mxkv_copy_run for them before any later write to the cache.
+ */
+typedef struct mxkv_pool_state* mxkv_pool;
+
+/* A pool of `pages` pages for `seqs` sequences, all empty, of at most cols pages each. MX_ERR_SHAPE: a
+ * value below 1 or above MX_MAX_DIM, or seqs * cols or pages * page_size of 2^31 or more. */
+int mxkv_pool_create(mxkv_pool* out, int pages, int page_size, int seqs, int cols);
+int mxkv_pool_destroy(mxkv_pool p);
+
+/* Set sequence `seq`'s length to `tokens`, taking pages at its end or giving them back. Where it grows
+ * and its last, partly filled page is shared, the sequence gets a copy of its own: pair[0] and pair[1]
+ * are the source and the copy and *n_pairs is 1 (else 0). MX_ERR_NOMEM: too few free pages (nothing
+ * has changed). MX_ERR_SHAPE: seq out of range, or tokens outside 0 .. cols * page_size. */
+int mxkv_pool_resize(mxkv_pool p, int seq, int tokens, int32_t pair[2], int* n_pairs);
+
+/* Let the empty sequence dst hold src's pages and length (MX_ERR_SHAPE if dst is not empty, or
+ * src == dst). Nothing is copied until one of them grows. */
+int mxkv_pool_fork(mxkv_pool p, int src, int dst);
+
+/* Reorder: sequence i becomes what sequence from[i] was, for all i at once (from: int32 [seqs]; several
+ * i may name one source, as when beams are chosen, and sources named by none are freed). */
+int mxkv_pool_reorder(mxkv_pool p, const int32_t* from);
+
+/* Move the used pages with the highest numbers into the free ones with the lowest until the used pages are
+ * 0 .. used - 1. Writes at most max_pairs moves to pairs and their number to *n_pairs (further calls
+ * go on); the tables name the new pages at once. */
+int mxkv_pool_compact(mxkv_pool p, int32_t* pairs, int max_pairs, int* n_pairs);
+
+/* The tables (int32 [seqs][cols], -1 where there is no page) and lengths (int32 [seqs]) in host memory
+ * owned by the pool, and the number of pages in use. NULL / 0 for a NULL pool. */
+const int32_t* mxkv_pool_table(mxkv_pool p);
+const int32_t* mxkv_pool_lengths(mxkv_pool p);
+int mxkv_pool_used(mxkv_pool p);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,331 @@
+"""Host side of the decode step's cache: frequency rules, refusals of every entry point (no GPU work is
+queued) and the page pool against a plain model."""
+import ctypes
+import math
+import random
+
+import numpy as np
+import pytest
+
+api = pytest.importorskip("block_scaled_quantized_amd.api")
+lib = api._lib
+
+
+# ---- frequency rules ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rot", [2, 20, 64, 128, 256])
+@pytest.mark.parametrize("rule,params", [("plain", ()), ("linear", (4.0,)), ("ntk", (8.0,)), ("bands", (8.0, 8192.0, 1.0, 4.0)),
+                                         ("yarn", (16.0, 4096.0, 32.0, 1.0))])
+def test_frequencies(rot, rule, params):
+    base = 10000.0
+    got, factor = api.mxrope_freqs_host(rot, base, getattr(api, "MXROPE_" + rule.upper()), params)
+    want = []
+    for i in range(rot // 2):
+        b = base * params[0] ** (rot / (rot - 2)) if rule == "ntk" and rot > 2 else base
+        f = b ** (-2 * i / rot)
+        if rule == "linear":
+            f /= params[0]
+        elif rule == "bands":
+            turns = params[1] * f / (2 * math.pi)
+            k = min(max((turns - params[2]) / (params[3] - params[2]), 0), 1)
+            f = (1 - k) * f / params[0] + k * f
+        elif rule == "yarn":
+            index = [rot * math.log(params[1] / (t * 2 * math.pi)) / (2 * math.log(base)) for t in params[2:]]
+            a, c = max(math.floor(index[0]), 0), min(math.ceil(index[1]), rot - 1)
+            r = min(max((i - a) / max(c - a, 0.001), 0), 1)
+            f = r * f / params[0] + (1 - r) * f
+        want.append(f)
+    assert len(got) == rot // 2
+    np.testing.assert_allclose(got, want, rtol=16 * 2.0 ** -53 * 64, atol=0)
+    assert factor == np.float32(0.1 * math.log(16.0) + 1 if rule == "yarn" else 1.0)
+
+
+@pytest.mark.parametrize("args,status", [
+    ((3, 1e4, 0, None), "SHAPE"), ((0, 1e4, 0, None), "SHAPE"), ((258, 1e4, 0, None), "SHAPE"), ((64, 0.0, 0, None), "SHAPE"),
+    ((64, math.inf, 0, None), "SHAPE"), ((64, math.nan, 0, None), "SHAPE"), ((64, 1e4, 5, None), "FORMAT"), ((64, 1e4, -1, None), "FORMAT"),
+    ((64, 1e4, 1, None), "NULL"), ((64, 1e4, 1, (0.0,)), "SHAPE"), ((64, 1e4, 2, (-1.0,)), "SHAPE"), ((64, 1e4, 1, (math.nan,)), "SHAPE"),
+    ((64, 1e4, 3, (8.0, 8192.0, 4.0, 4.0)), "SHAPE"), ((64, 1e4, 3, (8.0, 0.0, 1.0, 4.0)), "SHAPE"),
+    ((64, 1.0, 4, (8.0, 4096.0, 32.0, 1.0)), "SHAPE"), ((64, 1e4, 4, (8.0, 4096.0, 0.0, 1.0)), "SHAPE")])
+def test_frequency_refusals(args, status):
+    rot, base, rule, params = args
+    freq, factor = (ctypes.c_double * 128)(*([7.0] * 128)), ctypes.c_float(7.0)
+    par = (ctypes.c_double * 4)(*params) if params else None
+    assert lib.mxrope_freqs_host(rot, base, rule, par, freq, ctypes.addressof(factor)) == getattr(api, "MX_ERR_" + status)
+    assert set(freq) == {7.0} and factor.value == 7.0
+    assert lib.mxrope_freqs_host(64, 1e4, 0, None, None, ctypes.addressof(factor)) == api.MX_ERR_NULL
+
+
+# ---- refusals: addresses are never followed, so any aligned number stands for device memory ------
+
+P = 1 << 20
+
+
+def heads(data=P, n=8, token=8 * 128, head=128):
+    return api._Heads(data, n, token, head)
+
+
+def cache(**kw):
+    c = dict(fmt=api.MX_E4M3, order=0, pages=16, page_size=16, heads=8, dim=128, page_stride=16 * 8 * 128, k=P, v=2 * P, ks=3 * P, vs=4 * P)
+    c.update(kw)
+    return api._Cache(*[c[n] for n, _ in api._Cache._fields_])
+
+
+def at(x):
+    return ctypes.byref(x) if isinstance(x, (ctypes.Structure, ctypes.Array)) else x
+
+
+def rope(rot=128, layout=0, freq=P):
+    return api._Rope(rot, layout, freq, 1.0)
+
+
+BAD_HEADS = [(dict(data=None), "NULL"), (dict(data=P + 8), "ALIGN"), (dict(n=0), "SHAPE"), (dict(token=1020), "SHAPE"), (dict(head=129), "SHAPE")]
+BAD_ROPE = [(dict(freq=None), "NULL"), (dict(freq=P + 4), "ALIGN"), (dict(rot=0), "SHAPE"), (dict(rot=63), "SHAPE"), (dict(rot=130), "SHAPE"),
+            (dict(layout=2), "FORMAT")]
+BAD_CACHE = [(dict(fmt=api.MX_E5M2), "FORMAT"), (dict(fmt=api.MX_F32), "FORMAT"), (dict(order=2), "FORMAT"), (dict(pages=0), "SHAPE"),
+             (dict(page_size=0), "SHAPE"), (dict(pages=1 << 27), "SHAPE"), (dict(heads=0), "SHAPE"), (dict(heads=1025), "SHAPE"),
+             (dict(dim=0), "SHAPE"), (dict(dim=120), "SHAPE"), (dict(dim=288), "SHAPE"), (dict(page_stride=16 * 8 * 128 - 32), "SHAPE"),
+             (dict(page_stride=16 * 8 * 128 + 16), "SHAPE"), (dict(k=None), "NULL"), (dict(vs=None), "NULL"), (dict(v=P + 4), "ALIGN"),
+             (dict(ks=P + 1), "ALIGN")]
+
+
+def run_rope(f=api.MX_F16, r=None, tokens=4, dim=128, x=None, out=None, pos=P):
+    return lib.mxrope_run(f, at(r or rope()), tokens, dim, at(x or heads()), at(out or heads(2 * P)), pos, 0, None)
+
+
+def test_rope_refusals():
+    for kw, s in BAD_ROPE:
+        assert run_rope(r=rope(**kw)) == getattr(api, "MX_ERR_" + s), kw
+    for kw, s in BAD_HEADS:
+        assert run_rope(x=heads(**kw)) == getattr(api, "MX_ERR_" + s), kw
+        assert run_rope(out=heads(**kw)) == getattr(api, "MX_ERR_" + s), kw
+    assert run_rope(f=api.MX_E4M3) == api.MX_ERR_FORMAT
+    assert run_rope(f=api.MX_INT8) == api.MX_ERR_FORMAT
+    for kw in (dict(tokens=-1), dict(tokens=(1 << 20) + 1), dict(dim=4), dict(dim=264), dict(dim=100), dict(out=heads(2 * P, n=4)),
+               dict(x=heads(n=65537), out=heads(2 * P, n=65537)), dict(out=heads(P, token=2048))):
+        assert run_rope(**kw) == api.MX_ERR_SHAPE, kw
+    assert run_rope(pos=None) == api.MX_ERR_NULL
+    assert lib.mxrope_run(api.MX_F16, None, 4, 128, at(heads()), at(heads()), P, 0, None) == api.MX_ERR_NULL
+    assert lib.mxrope_run(api.MX_F16, at(rope()), 4, 128, None, at(heads()), P, 0, None) == api.MX_ERR_NULL
+    assert run_rope(tokens=0, pos=None, x=heads(None), out=heads(None)) == api.MX_OK   # an empty call needs no memory
+
+
+def run_append(c=None, f=api.MX_F16, tokens=4, k=None, v=None, pos=P, seq=None, table=None, r=None, q=None, q_out=None):
+    return lib.mxkv_append_run(at(c or cache()), f, tokens, at(k or heads()), at(v or heads(2 * P)), pos, seq,
+                               at(table or api._Table(P, 4, 8)), at(r), at(q), at(q_out), None)
+
+
+def test_append_refusals():
+    for kw, s in BAD_CACHE:
+        assert run_append(c=cache(**kw)) == getattr(api, "MX_ERR_" + s), kw
+    for kw, s in BAD_HEADS:
+        assert run_append(k=heads(**kw)) == getattr(api, "MX_ERR_" + s), kw
+        assert run_append(v=heads(**kw)) == getattr(api, "MX_ERR_" + s), kw
+        assert run_append(r=rope(), q=heads(**kw), q_out=heads()) == getattr(api, "MX_ERR_" + s), kw
+        assert run_append(r=rope(), q=heads(5 * P), q_out=heads(**kw)) == getattr(api, "MX_ERR_" + s), kw
+    for kw, s in BAD_ROPE:
+        assert run_append(r=rope(**kw)) == getattr(api, "MX_ERR_" + s), kw
+    for f in (api.MX_F32, api.MX_E4M3):
+        assert run_append(f=f) == api.MX_ERR_FORMAT
+    assert run_append(c=cache(fmt=api.MX_BF16, ks=None, vs=None)) == api.MX_ERR_FORMAT      # fp16 into a bf16 cache
+    for kw in (dict(tokens=-1), dict(k=heads(n=4)), dict(v=heads(n=16)), dict(table=api._Table(P, -1, 8)), dict(table=api._Table(P, 4, 0)),
+               dict(r=rope(), q=heads(5 * P, n=16), q_out=heads(6 * P))):
+        assert run_append(**kw) == api.MX_ERR_SHAPE, kw
+    for kw in (dict(pos=None), dict(table=api._Table(None, 4, 8)), dict(r=rope(), q=heads()), dict(r=rope(), q_out=heads()),
+               dict(q=heads(), q_out=heads())):
+        assert run_append(**kw) == api.MX_ERR_NULL, kw
+    assert run_append(tokens=0, pos=None) == api.MX_OK
+
+
+def run_attn(c=None, f=api.MX_F16, q=None, out=None, table=None, lengths=P, max_len=64, opts=None, ws=None, ws_bytes=0):
+    return lib.mxattn_decode_run(at(c or cache()), f, at(q or heads(n=32)), at(out or heads(2 * P, n=32)), None,
+                                 at(table or api._Table(P, 4, 8)), lengths, None, max_len, at(opts or api._AttnOpts(1.0, 0.0, 0)), ws, ws_bytes, None)
+
+
+def test_attention_refusals():
+    for kw, s in BAD_CACHE:
+        assert run_attn(c=cache(**kw)) == getattr(api, "MX_ERR_" + s), kw
+    for kw, s in BAD_HEADS:
+        assert run_attn(q=heads(**dict(dict(n=32), **kw)), out=heads(n=kw.get("n", 32))) == getattr(api, "MX_ERR_" + s), kw
+        assert run_attn(out=heads(**dict(dict(n=32), **kw))) == getattr(api, "MX_ERR_" + s), kw
+    assert run_attn(f=api.MX_F32) == api.MX_ERR_FORMAT
+    assert run_attn(c=cache(fmt=api.MX_F16), f=api.MX_BF16) == api.MX_ERR_FORMAT
+    opts = api._AttnOpts
+    for kw in (dict(q=heads(n=12), out=heads(n=12)), dict(max_len=0), dict(max_len=1 << 30), dict(opts=opts(math.nan, 0.0, 0)),
+               dict(opts=opts(1.0, -1.0, 0)), dict(opts=opts(1.0, math.inf, 0)), dict(opts=opts(1.0, 0.0, -1)), dict(table=api._Table(P, -1, 8)),
+               dict(table=api._Table(P, 1 << 20, 8))):
+        assert run_attn(**kw) == api.MX_ERR_SHAPE, kw
+    assert run_attn(lengths=None) == api.MX_ERR_NULL
+    assert run_attn(table=api._Table(None, 4, 8)) == api.MX_ERR_NULL
+    assert run_attn(ws=P + 8, ws_bytes=1 << 20) == api.MX_ERR_ALIGN
+    assert run_attn(table=api._Table(None, 0, 8), lengths=None) == api.MX_OK
+
+
+def test_attention_workspace_size():
+    def size(seqs, q_heads, max_len, window=0, **kw):
+        return lib.mxattn_decode_workspace_size(at(cache(**kw)), seqs, q_heads, max_len, window)
+    assert size(1, 32, 128) == 0 and size(0, 32, 4096) == 0 and size(1, 12, 4096) == 0 and size(1, 32, 4096, dim=100) == 0
+    assert size(1, 32, 1 << 17) > size(1, 32, 4096) > 0
+    assert lib.mxattn_decode_workspace_size(None, 1, 32, 4096, 0) == 0
+    for seqs in (1, 3, 40, 1000):                 # a workspace for the longest row serves every window
+        full = size(seqs, 32, 40000)
+        assert all(size(seqs, 32, 40000, w) <= full for w in range(1, 40000, 997))
+
+
+def test_copy_refusals():
+    def run(layers, n_layers=None, pairs=P, n=3):
+        arr = (api._Cache * max(1, len(layers)))(*layers)
+        return lib.mxkv_copy_run(at(arr), len(layers) if n_layers is None else n_layers, pairs, n, None)
+    for kw, s in BAD_CACHE:
+        assert run([cache(), cache(**kw)]) in (getattr(api, "MX_ERR_" + s),), kw
+    for kw in (dict(order=1), dict(pages=15), dict(page_stride=16 * 8 * 128 + 32), dict(fmt=api.MX_F16), dict(dim=96), dict(heads=4),
+               dict(page_size=8)):
+        assert run([cache(), cache(**kw)]) == api.MX_ERR_SHAPE, kw
+    assert run([cache()], n=-1) == api.MX_ERR_SHAPE and run([cache()], n_layers=-1) == api.MX_ERR_SHAPE
+    assert run([cache()], pairs=None) == api.MX_ERR_NULL
+    assert lib.mxkv_copy_run(None, 1, P, 1, None) == api.MX_ERR_NULL
+    assert run([cache()], n=0, pairs=None) == api.MX_OK and run([], pairs=None) == api.MX_OK
+
+
+def test_no_device_is_an_error():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("needs a machine without a GPU")
+    assert run_rope() == api.MX_ERR_ARCH
+    assert run_append() == api.MX_ERR_ARCH
+    assert run_attn() == api.MX_ERR_ARCH
+    arr = (api._Cache * 1)(cache())
+    assert lib.mxkv_copy_run(at(arr), 1, P, 1, None) == api.MX_ERR_ARCH
+
+
+def test_python_refusals():
+    import torch
+    x = torch.zeros(4, 8, 128, dtype=torch.float16)
+    r, pos = api.Rope(128, P), torch.zeros(4, dtype=torch.int32)
+    for bad in (dict(x=x.transpose(1, 2)), dict(out=x[:2]), dict(positions=pos.long()), dict(positions=pos[:3])):
+        kw = dict(x=x, out=x, positions=pos)
+        kw.update(bad)
+        with pytest.raises(api.MXError) as e:
+            api.mxrope_run(api.MX_F16, r, kw["x"], kw["out"], kw["positions"], stream=0)
+        assert e.value.status == api.MX_ERR_SHAPE
+    k = torch.zeros(5, 2, 16, 64, dtype=torch.float16)
+    api.KVCache(api.MX_F16, k, k)
+    for bad in (k[:4], k.transpose(1, 2), torch.zeros(5, 2, 16, 32)):
+        with pytest.raises(api.MXError):
+            api.KVCache(api.MX_F16, k, bad)
+    with pytest.raises(api.MXError):
+        api.KVCache(api.MX_E4M3, k, k, k[..., :1], k[..., :1])
+    both = torch.zeros(5, 2, 2, 16, 64, dtype=torch.float16)           # keys and values in one allocation
+    assert api.KVCache(api.MX_F16, both[:, 0], both[:, 1]).c.page_stride == 2 * 2 * 16 * 64
+
+
+# ---- page pool -----------------------------------------------------------------------------------
+
+class Model:
+    """The pool's rules, plainly: rows of pages, the lowest free page first."""
+
+    def __init__(self, pages, page, seqs, cols):
+        self.n, self.page, self.rows, self.len, self.cols = pages, page, [[] for _ in range(seqs)], [0] * seqs, cols
+
+    def held(self):
+        return {p for r in self.rows for p in r}
+
+    def free(self):
+        return [p for p in range(self.n) if p not in self.held()]
+
+    def shared(self, p):
+        return sum(p in r for r in self.rows) > 1
+
+    def resize(self, s, t):
+        row, need, pairs = self.rows[s], -(-t // self.page), []
+        own = t > self.len[s] and self.len[s] % self.page and self.shared(row[-1])
+        if max(0, need - len(row)) + bool(own) > len(self.free()):
+            return None
+        if own:
+            to = self.free()[0]
+            pairs, row[-1] = [(row[-1], to)], to
+        while len(row) < need:
+            row.append(self.free()[0])
+        del row[need:]
+        self.len[s] = t
+        return pairs
+
+    def compact(self, most):
+        pairs, held = [], self.held()
+        while len(pairs) < most:
+            hole, top = min(set(range(self.n)) - held, default=self.n), max(held, default=-1)
+            if hole > top:
+                break
+            pairs.append((top, hole))
+            held = held - {top} | {hole}
+            self.rows = [[hole if p == top else p for p in r] for r in self.rows]
+        return pairs
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_pool_follows_the_model(seed):
+    r = random.Random(seed)
+    pages, page, seqs, cols = r.choice([(7, 4, 3, 4), (40, 1, 6, 9), (64, 16, 9, 12)])
+    pool, m = api.KVPool(pages, page, seqs, cols), Model(pages, page, seqs, cols)
+    moved = {p: p for p in range(pages)}
+    for _ in range(300):
+        do = r.random()
+        s = r.randrange(seqs)
+        if do < 0.6:
+            t = r.choice([0, m.len[s] + 1, r.randint(0, cols * page)])
+            if t > cols * page:
+                continue
+            want = m.resize(s, t)
+            if want is None:
+                with pytest.raises(api.MXError) as e:
+                    pool.resize(s, t)
+                assert e.value.status == api.MX_ERR_NOMEM
+            else:
+                assert pool.resize(s, t) == want
+        elif do < 0.8:
+            d = r.randrange(seqs)
+            if s != d and not m.len[d]:
+                pool.fork(s, d)
+                m.rows[d], m.len[d] = list(m.rows[s]), m.len[s]
+            else:
+                with pytest.raises(api.MXError):
+                    pool.fork(s, d)
+        elif do < 0.9:
+            order = [r.randrange(seqs) for _ in range(seqs)]
+            pool.reorder(order)
+            m.rows, m.len = [list(m.rows[i]) for i in order], [m.len[i] for i in order]
+        else:
+            most = r.choice([0, 1, 3, pages])
+            assert pool.compact(most) == m.compact(most)
+        assert pool.lengths().tolist() == m.len and pool.used == len(m.held())
+        assert pool.table().tolist() == [row + [-1] * (cols - len(row)) for row in m.rows]
+    pool.compact()
+    assert pool.table().max() < pool.used
+    pool.close()
+
+
+def test_pool_refusals():
+    h = ctypes.c_void_p()
+    for args in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0), ((1 << 20) + 1, 1, 1, 1), (1 << 20, 1 << 20, 1, 1),
+                 (1, 1, 1 << 20, 1 << 20), (1, 1 << 20, 1, 1 << 20)):
+        assert lib.mxkv_pool_create(ctypes.byref(h), *args) == api.MX_ERR_SHAPE and not h.value, args
+    assert lib.mxkv_pool_create(None, 1, 1, 1, 1) == api.MX_ERR_NULL
+    pool = api.KVPool(4, 16, 2, 3)
+    for seq, t in ((-1, 1), (2, 1), (0, -1), (0, 49)):
+        with pytest.raises(api.MXError) as e:
+            pool.resize(seq, t)
+        assert e.value.status == api.MX_ERR_SHAPE
+    assert pool.resize(0, 48) == [] and pool.used == 3
+    with pytest.raises(api.MXError) as e:
+        pool.resize(1, 32)
+    assert e.value.status == api.MX_ERR_NOMEM and pool.used == 3 and pool.lengths().tolist() == [48, 0]
+    with pytest.raises(api.MXError):
+        pool.reorder([0, 2])
+    with pytest.raises(api.MXError):
+        pool.reorder([0])
+    n, pair = ctypes.c_int(), (ctypes.c_int32 * 2)()
+    assert lib.mxkv_pool_resize(None, 0, 1, pair, ctypes.byref(n)) == api.MX_ERR_NULL
+    assert lib.mxkv_pool_resize(pool.handle, 0, 1, None, ctypes.byref(n)) == api.MX_ERR_NULL
+    assert lib.mxkv_pool_compact(pool.handle, None, 2, ctypes.byref(n)) == api.MX_ERR_NULL
+    assert lib.mxkv_pool_compact(pool.handle, pair, -1, ctypes.byref(n)) == api.MX_ERR_SHAPE
+    assert lib.mxkv_pool_fork(None, 0, 1) == lib.mxkv_pool_reorder(None, pair) == api.MX_ERR_NULL
+    assert lib.mxkv_pool_table(None) is None and lib.mxkv_pool_used(None) == 0 and lib.mxkv_pool_destroy(None) == api.MX_OK
