@@ -18,6 +18,8 @@
 //
 // E4M3 elements become 16-bit ones on the way by gfx950's scaled conversion, which takes the block's
 // power of two: a lane's 8 K elements and its V elements of one key lie in one block of 32.
+#include <algorithm>
+
 #include "kvcache.h"
 
 using namespace mx;
@@ -36,6 +38,9 @@ constexpr int kLeast = 2;                // grains: no unit is cut within this o
 constexpr int kFan = 128, kGroup = 64;   // partials that one workgroup joins; groups of more
 constexpr int kDeep = 16;                // partials that a joining thread has on their way
 constexpr int kPad = 4;                  // floats that keep the heads' rows of the merge on different banks
+// Keys and values are read once: marked non-temporal, they leave the L2 to the program, whose prologue and
+// joins otherwise wait for their instructions (131072 x 8 x 128 fp16: 114 -> 103 us).
+constexpr int kStream = 2;
 constexpr int kFar = 1 << 30;            // a byte offset past every buffer: loads give 0
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -48,10 +53,10 @@ struct Args {
   uint32_t* counters;
   float* partial;
   int64_t qt, qh, ot, oh, page_stride, head_stride, slot_stride;
-  int seqs, heads, group, tiles, dim, cols, pages, page_size, max_len, window, wgs;
+  int seqs, heads, group, tiles, dim, cols, pages, page_size, max_len, max_keys, window, wgs;
   bool split;
   float scale, softcap;
-  FastDiv page_div;
+  FastDiv page_div, units_div, wgs_div, quads_div;  // units: of one sequence
 };
 
 template <typename T>
@@ -97,8 +102,10 @@ MX_DEV float wave_max(float x) {
   return fmaxf(bitsf(r[0]), bitsf(r[1]));
 }
 MX_DEV float wave_sum(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  auto r = __builtin_amdgcn_permlane16_swap(fbits(x), fbits(x), false, false);
+  x = bitsf(r[0]) + bitsf(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(fbits(x), fbits(x), false, false);
+  return bitsf(r[0]) + bitsf(r[1]);
 }
 MX_DEV float finite_or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -117,109 +124,134 @@ MX_DEV f32x4 get4(rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 17));
 }
 
+// The kernel's arguments where the launch left them. A phase that reads them through a fresh() pointer has
+// them loaded anew (a hit of the scalar cache) instead of held in scalar registers since the kernel's start,
+// which are too few for that.
+typedef const __attribute__((address_space(4))) Args Kernarg;
+MX_DEV Kernarg* fresh(Kernarg* p) {
+  asm("" : "+s"(p));
+  return p;
+}
+MX_DEV FastDiv copy_of(const __attribute__((address_space(4))) FastDiv& d) {
+  FastDiv f;
+  f.m = d.m, f.d = d.d, f.s = d.s;
+  return f;
+}
+
 // One sequence's attended positions lo .. hi - 1, counted in grains from the tile that holds lo. A row
 // without positions still has a grain, whose workgroup writes it.
 struct Row {
   int lo, hi, base, grains;
 };
 
-MX_DEV Row row_of(const Args& a, int b) {
+MX_DEV Row row_of(Kernarg& a, int length, int start) {
   Row r;
-  r.hi = max(0, min(min(a.lengths[b], a.max_len), (int)min((int64_t)a.cols * a.page_size, (int64_t)INT32_MAX)));
-  r.lo = a.starts ? max(a.starts[b], 0) : 0;
+  r.hi = max(0, min(min(length, a.max_len), a.max_keys));
+  r.lo = max(start, 0);
   if (a.window > 0) r.lo = max(r.lo, r.hi - a.window);
   if (r.lo >= r.hi) r.lo = r.hi = 0;
   r.base = r.lo & ~(kTile - 1);
-  r.grains = max(1, ceil_div(r.hi - r.base, kGrain));
+  r.grains = max(1, (r.hi - r.base + kGrain - 1) / kGrain);
   return r;
 }
+MX_DEV Row row_of(Kernarg& a, int b) { return row_of(a, a.lengths[b], a.starts ? a.starts[b] : 0); }
 
 MX_DEV int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-MX_DEV int64_t uniform64(int64_t x) {
-  return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
+
+// Sum over the lanes up to this one: within rows of 16, then over the rows.
+MX_DEV uint32_t wave_scan(uint32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // lane 15 of a row to the next row
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // lane 31 to the upper half
+  return x;
 }
-MX_DEV uint64_t quotient(uint64_t n, uint64_t d) { return (n | d) >> 32 ? n / d : (uint32_t)n / (uint32_t)d; }
 
 // A place in the list of all units' grains: sequence, unit within it, grain; `at` numbers the sequence's
 // first grain.
 struct Place {
   int b, unit, grain;
-  int64_t at;
+  uint32_t at;
 };
 
-// This workgroup's share of the grains, from..to, of equal size but for the cuts' distance from the
-// units' ends. Every workgroup sums up the lengths by itself: a handful of loads that all of them find in
-// the caches, where a launch that planned would cost its own latency.
-MX_DEV int64_t share_of(const Args& a, Place& from, Place& to) {
-  __shared__ uint32_t wave_total[kWaves];
-  __shared__ Place place[2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, units = a.heads * a.tiles;
-  const auto scan = [&](uint32_t n, uint32_t& total) -> uint32_t {  // sum of the lower threads' n
-    uint32_t s = n;
+// This workgroup's share of the grains, from..to, of equal size (which is returned) but for the cuts'
+// distance from the units' ends. Every wave sums up the lengths by itself, four neighbouring sequences to a
+// lane: a handful of loads that all find in the caches, where a launch that planned would cost its own
+// latency, and no barrier.
+MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
+  constexpr int kEach = 4, kLook = 64 * kEach;
+  const int lane = threadIdx.x & 63;
+  uint32_t n[kEach], own, before, total;
+  const auto look = [&](int b0) {
+    own = 0u;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const uint32_t o = __shfl_up(s, d);
-      s += lane >= d ? o : 0u;
+    for (int i = 0; i < kEach; i++) {
+      const int b = b0 + kEach * lane + i;
+      n[i] = b < a.seqs ? (uint32_t)row_of(a, b).grains : 0u;
+      own += n[i];
     }
-    __syncthreads();
-    if (lane == 63) wave_total[wave] = s;
-    __syncthreads();
-    uint32_t before = 0u;
-    total = 0u;
-#pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-      const uint32_t t = wave_total[w];
-      before += w < wave ? t : 0u;
-      total += t;
-    }
-    return before + s - n;
+    before = wave_scan(own);
+    total = (uint32_t)__builtin_amdgcn_readlane((int)before, 63);
+    before -= own;
   };
-  const auto grains_of = [&](int b) -> uint32_t { return b < a.seqs ? (uint32_t)row_of(a, b).grains : 0u; };
-  int64_t all = 0;
-  uint32_t total, n = grains_of(threadIdx.x), before = scan(n, total);
-  all = total;
-  for (int b = kThreads; b < a.seqs; b += kThreads) {
-    scan(grains_of(b + threadIdx.x), total);
+  look(0);
+  uint32_t all = total;
+  for (int b0 = kLook; b0 < a.seqs; b0 += kLook) {
+    look(b0);
     all += total;
   }
-  const int64_t per = max((int64_t)kLeast, (int64_t)quotient((uint64_t)(all * units + a.wgs - 1), (uint64_t)a.wgs));
-  const int64_t cut[2] = {blockIdx.x * per, (blockIdx.x + 1) * per};
-  if (threadIdx.x < 2) place[threadIdx.x] = Place{a.seqs, 0, 0, all * units};
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < a.seqs; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    if (a.seqs > kThreads) {
-      n = grains_of(b);
-      before = scan(n, total);
-    } else {
-      __syncthreads();
-    }
-    const int64_t at = (sum + before) * units;
+  all *= (uint32_t)units;  // below 2^31
+  const uint32_t per = max((uint32_t)kLeast, copy_of(a.wgs_div).div(all + (uint32_t)a.wgs - 1u));
+  uint32_t sum = 0u;
+  from = to = Place{a.seqs, 0, 0, all};
+  for (int b0 = 0; b0 < a.seqs; b0 += kLook) {
+    if (a.seqs > kLook) look(b0);
+#pragma unroll 1
+    for (int side = 0; side < 2; side++) {
+      const uint32_t cut = min(all, (blockIdx.x + side) * per);
+      const uint32_t q = copy_of(a.units_div).div(cut) - sum;  // grains of a unit's column before the cut's
+      if (cut >= all || q >= total) continue;  // (a cut before this block wraps around)
+      // the last lane that starts at or before q, and the sequence among its four
+      const int at_lane = 63 - __builtin_clzll(__ballot(before <= q));
+      uint32_t start = (uint32_t)__builtin_amdgcn_readlane((int)before, at_lane), size = 0u;
+      int b = b0 + kEach * at_lane;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      if (n == 0u || cut[i] < at || cut[i] >= at + (int64_t)n * units) continue;
-      Place p = {b, (int)quotient((uint64_t)(cut[i] - at), n), 0, at};
-      p.grain = (int)(cut[i] - at - (int64_t)p.unit * n);
+      for (int i = 0; i < kEach; i++) {
+        const uint32_t next = (uint32_t)__builtin_amdgcn_readlane((int)n[i], at_lane);
+        if (i == 0 || q >= start + size) {
+          if (i) b++, start += size;
+          size = next;
+        }
+      }
+      Place p = {b, 0, 0, (sum + start) * units};
+      p.unit = uniform((int)((cut - p.at) / size));
+      p.grain = (int)(cut - p.at - p.unit * size);
       if (p.grain < kLeast) p.grain = 0;
-      else if ((int)n - p.grain < kLeast) p.grain = 0, p.unit++;
-      if (p.unit == units) p = Place{b + 1, 0, 0, at + (int64_t)n * units};
-      place[i] = p;
+      else if ((int)size - p.grain < kLeast) p.grain = 0, p.unit++;
+      if (p.unit == units) p = Place{b + 1, 0, 0, p.at + size * units};
+      if (side) to = p;
+      else from = p;
     }
     sum += total;
   }
-  __syncthreads();
-  from = place[0], to = place[1];
-  from = Place{uniform(from.b), uniform(from.unit), uniform(from.grain), uniform64(from.at)};
-  to = Place{uniform(to.b), uniform(to.unit), uniform(to.grain), uniform64(to.at)};
-  return uniform64(per);
+  return per;
+}
+
+// c tanh(s / c) by one exponential: its error is relative to c, which is what a score's counts for.
+MX_DEV float soft_cap(float s, float c) {
+  const float e = __builtin_amdgcn_exp2f(s * fminf(2.0f * kLog2e / c, 3.0e38f));
+  return c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // D: 64, 128 or 256, the head size rounded up. T: type of q, out and the arithmetic. MX8: E4M3 cache.
 // PAGED16: page_size % 16 == 0, so that the 16 keys of half a tile lie in one page: their place is a
 // buffer descriptor in scalar registers, whose size also turns keys past the end, missing pages and
-// elements past dim into zeros. Other page sizes look every key's page up in the lanes.
+// elements past dim into zeros. For other page sizes a lane works out one key's place and the others
+// read it from LDS.
 template <int D, typename T, bool MX8, bool PAGED16>
-__global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args) {
   typedef typename Vec<T>::x8 x8;
   constexpr float kShift = Vec<T>::kShift;
   constexpr int kSteps = D / 32;          // matrix instructions of one score tile
@@ -232,44 +264,31 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
   extern __shared__ float lds[];          // merge: [kWaves / 2][head][D + kPad]; join: sums, then [head][kFan] weights
   __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
   __shared__ int is_last;
+  __shared__ int64_t place_of[PAGED16 ? 1 : kWaves][2][kTile];  // of the keys of a wave's two tiles
 
+  Kernarg* const args = (Kernarg*)__builtin_amdgcn_kernarg_segment_ptr();
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
-  const int units = a.heads * a.tiles, quads = a.dim / 4;
+  const int units = args->heads * args->tiles;
   Place at, end;
-  int64_t per = 1;
-  if (a.split) {
-    per = share_of(a, at, end);
+  uint32_t per = 1u;
+  if (args->split) {
+    per = share_of(*args, units, at, end);
   } else {
-    at = Place{(int)blockIdx.x / units, (int)blockIdx.x % units, 0, 0};
+    const int b = (int)copy_of(args->units_div).div(blockIdx.x);
+    at = Place{b, (int)blockIdx.x - b * units, 0, 0};
     end = at.unit + 1 < units ? Place{at.b, at.unit + 1, 0, 0} : Place{at.b + 1, 0, 0, 0};
   }
 
-  // Byte offsets of this lane's loads within 16 keys' rows.
-  const int slot_bytes = (int)a.slot_stride * kSize, slot_scales = (int)a.slot_stride / 32;
-  int k_at[kLoads], v_at[4][kRuns];
-#pragma unroll
-  for (int s = 0; s < kLoads; s++) {
-    const int d = MX8 ? 64 * s + 16 * g : 32 * s + 8 * g;
-    k_at[s] = d < a.dim ? c * slot_bytes + d * kSize : kFar;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; j++)
-#pragma unroll
-    for (int r = 0; r < kRuns; r++) {
-      const int d = 128 * r + kRow * c;
-      v_at[j][r] = d < a.dim ? (4 * g + j) * slot_bytes + d * kSize : kFar;
-    }
-
   while (at.b < end.b || (at.b == end.b && (at.unit < end.unit || (at.unit == end.unit && at.grain < end.grain)))) {
-    const int b = at.b;
-    Row row = row_of(a, b);
-    row = Row{uniform(row.lo), uniform(row.hi), uniform(row.base), uniform(row.grains)};
+    Kernarg& a = *fresh(args);
+    const int b = at.b, dim = a.dim;
     const int ht = at.unit % a.tiles, hk = at.unit / a.tiles;
     const int first_head = hk * a.group + 16 * ht, n_heads = min(16, a.group - 16 * ht);
-    const int stop = b == end.b && at.unit == end.unit ? end.grain : row.grains;
-    const int from = row.base + at.grain * kGrain, to = min(row.hi, row.base + stop * kGrain), lo = row.lo;
-    const int64_t head_at = (int64_t)hk * a.head_stride;
+    const int64_t head_at = (int64_t)hk * a.head_stride, page_stride = a.page_stride, slot_stride = a.slot_stride;
     const int32_t* table = a.table + (int64_t)b * a.cols;
+    const FastDiv page_div = copy_of(a.page_div);
+    const int page_size = a.page_size, pages = a.pages, cols = a.cols;
+    const float score_scale = a.scale, softcap = a.softcap;
 
     // Query fragments: column c, the elements that this lane's K loads hold.
     x8 qf[kSteps];
@@ -277,171 +296,184 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
     for (int s = 0; s < kSteps; s++) {
       const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
       u32x4 w = {0u, 0u, 0u, 0u};
-      if (c < n_heads && d < a.dim)
+      if (c < n_heads && d < dim)
         w = *reinterpret_cast<const u32x4*>((const T*)a.q + (int64_t)b * a.qt + (int64_t)(first_head + c) * a.qh + d);
       qf[s] = __builtin_bit_cast(x8, w);
     }
+
+    // The page of a key, -1 where there is none. A page number is read before the length that says whether the
+    // key counts has come, so that the two loads wait together.
+    const auto page_at = [&](int index) -> int {
+      const int p = table[min(index, cols - 1)];
+      return p >= 0 && p < pages ? p : -1;
+    };
+    const bool from_zero = !a.starts && a.window == 0;
+    const int ahead = at.grain * kGrain + wave * kTile;  // the wave's first key, if the row starts at 0
+    int page_ahead = -1;
+    if (from_zero) page_ahead = page_at((int)page_div.div((uint32_t)(ahead + (PAGED16 ? (lane >> 1) * kGrain + (lane & 1) * 16 : lane & (kTile - 1)))));
+    Row row = row_of(a, b);
+    row = Row{uniform(row.lo), uniform(row.hi), from_zero ? 0 : uniform(row.base), uniform(row.grains)};
+    const int stop = b == end.b && at.unit == end.unit ? end.grain : row.grains;
+    const int from = row.base + at.grain * kGrain, to = min(row.hi, row.base + stop * kGrain), lo = row.lo;
+
+    // Byte offsets of this lane's loads within 16 keys' rows.
+    const int slot_bytes = (int)slot_stride * kSize, slot_scales = (int)slot_stride / 32;
+    int k_at[kLoads], v_at[4][kRuns];
+#pragma unroll
+    for (int s = 0; s < kLoads; s++) {
+      const int d = MX8 ? 64 * s + 16 * g : 32 * s + 8 * g;
+      k_at[s] = d < dim ? c * slot_bytes + d * kSize : kFar;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+      for (int r = 0; r < kRuns; r++) {
+        const int d = 128 * r + kRow * c;
+        v_at[j][r] = d < dim ? (4 * g + j) * slot_bytes + d * kSize : kFar;
+      }
+    const uint8_t *kp = a.k, *vp = a.v, *ksp = a.ks, *vsp = a.vs;
 
     f32x4 acc[kOut];
 #pragma unroll
     for (int i = 0; i < kOut; i++) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
 
-    u32x4 kw[2][kLoads], vw[8][kRuns];
-    u32x2 vc[8][kRuns];
-    uint32_t ke[2][kLoads], ve[8][kRuns];
+    // Two tiles are on their way: a tile's K is loaded again as soon as its scores are formed, its V
+    // as soon as it is added up.
+    struct Tile {
+      u32x4 k[2][kLoads], v[8][kRuns];
+      uint32_t ke[2][kLoads], ve[8][kRuns];
+      int64_t off[2];        // PAGED16: element offset of each half's page slot, and its keys
+      int rows[2];
+      uint32_t mask;         // not PAGED16: bit i: key i is attended
+    } tile[2];
     for (int first = from + wave * kTile; first < to; first += kBlock * kGrain) {
-      const int upto = min(to, first + kBlock * kGrain);  // the next tiles of this block end here
-      const int n_tiles = ceil_div(upto - first, kGrain);
+      const int upto = min(to, first + kBlock * kGrain);  // the tiles of this block end here
+      const int n_tiles = (upto - first + kGrain - 1) / kGrain;
 
       // PAGED16: lane i holds the element offset of half i % 2 of tile i / 2 (negative: no page).
       int off_lo = 0, off_hi = -1;
-      // else: lane i holds the i-th page from the tile's first one, here and in the next tile
-      int page = -1, page_next = -1;
-      const auto lookup = [&](int index) -> int {
-        const int p = table[index];
-        return p >= 0 && p < a.pages ? p : -1;
-      };
-      const auto fetch_pages = [&](int t) -> int {  // of the tile at key t
-        const int i = (int)a.page_div.div((uint32_t)min(t, to - 1)) + lane, last = (int)a.page_div.div((uint32_t)(to - 1));
-        return i <= last && lane <= kTile ? lookup(i) : -1;
+      // else: lane i % 32 holds the page of key i of the next tile to be placed
+      int page = -1;
+      const auto fetch_page = [&](int it) -> int {
+        return page_at((int)page_div.div((uint32_t)min(first + it * kGrain + (lane & (kTile - 1)), to)));
       };
       if constexpr (PAGED16) {
-        const int key = first + (lane >> 1) * kGrain + (lane & 1) * 16;
-        if (key < upto) {
-          const int i = (int)a.page_div.div((uint32_t)key), p = lookup(i);
-          const int64_t off = p * a.page_stride + (key - i * a.page_size) * a.slot_stride + head_at;
-          off_lo = (int)off, off_hi = p < 0 ? -1 : (int)(off >> 32);
-        }
+        const int key = first + (lane >> 1) * kGrain + (lane & 1) * 16, i = (int)page_div.div((uint32_t)key);
+        const int p = from_zero && first == ahead ? page_ahead : page_at(i);
+        const int64_t off = p * page_stride + (key - i * page_size) * slot_stride + head_at;
+        off_lo = (int)off, off_hi = p < 0 ? -1 : (int)(off >> 32);
       } else {
-        page = fetch_pages(first);
+        page = from_zero && first == ahead ? page_ahead : fetch_page(0);
       }
 
-      int rows[2] = {0, 0};           // PAGED16: keys of each half of the tile whose K is loaded
-      int64_t off[2] = {0, 0};
-      uint32_t seen = 0u, seen_now;   // bit 4 h + i: key 16 h + 4 g + i of the tile is attended (not PAGED16)
-      const auto place_tile = [&](int it) {
+      const auto place_tile = [&](Tile& z, int it) {
         if constexpr (PAGED16) {
 #pragma unroll
           for (int h = 0; h < 2; h++) {
             const int hi = __builtin_amdgcn_readlane(off_hi, 2 * it + h), lw = __builtin_amdgcn_readlane(off_lo, 2 * it + h);
-            off[h] = (int64_t)((uint64_t)(uint32_t)max(hi, 0) << 32 | (uint32_t)lw);
-            rows[h] = hi < 0 ? 0 : min(16, max(0, upto - (first + it * kGrain + 16 * h)));
-          }
-        }
-      };
-      // Element offset of a key's row, and whether it is attended; others read the cache's first row, memory
-      // that is there and values that are dropped.
-      const auto row_at = [&](int t, int key, bool& ok) -> int64_t {
-        ok = key >= lo && key < upto;
-        const int at = ok ? key : t, i = (int)a.page_div.div((uint32_t)at);
-        const int p = __shfl(page, i - (int)a.page_div.div((uint32_t)t));
-        ok = ok && p >= 0;
-        return ok ? p * a.page_stride + (at - i * a.page_size) * a.slot_stride + head_at : head_at;
-      };
-      const auto load_k = [&](int it) {
-        if constexpr (PAGED16) {
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(a.k + off[h] * kSize), (short)0, rows[h] * slot_bytes, 0x00020000);
-#pragma unroll
-            for (int s = 0; s < kLoads; s++) kw[h][s] = __builtin_amdgcn_raw_buffer_load_b128(r, k_at[s], 0, 0);
-            if constexpr (MX8) {
-              const rsrc_t e = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ks + (off[h] >> 5)), (short)0, rows[h] * slot_scales, 0x00020000);
-#pragma unroll
-              for (int s = 0; s < kLoads; s++) ke[h][s] = __builtin_amdgcn_raw_buffer_load_b8(e, k_at[s] >> 5, 0, 0);
-            }
+            z.off[h] = (int64_t)((uint64_t)(uint32_t)max(hi, 0) << 32 | (uint32_t)lw);
+            z.rows[h] = hi < 0 ? 0 : uniform(min(16, max(0, upto - (first + it * kGrain + 16 * h))));  // a clamp is a vector instruction
           }
         } else {
-          const int t = min(first + it * kGrain, to - 1);
+          // keys that do not count have the cache's first row: memory that is there, and values that are dropped
+          const int key = first + it * kGrain + (lane & (kTile - 1));
+          const bool ok = key >= lo && key < upto && page >= 0;
+          const int64_t off = page * page_stride + (key - (int)page_div.div((uint32_t)key) * page_size) * slot_stride;
+          if (lane < kTile) place_of[wave][it & 1][lane] = head_at + (ok ? off : 0);
+          z.mask = (uint32_t)__ballot(ok);
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          page = fetch_page(it + 1);
+        }
+      };
+      const auto load_k = [&](Tile& z, int it) {
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            bool ok;
-            const int64_t o = row_at(t, first + it * kGrain + 16 * h + c, ok);
+        for (int h = 0; h < 2; h++) {
+          if constexpr (PAGED16) {
+            const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(kp + z.off[h] * kSize), (short)0, z.rows[h] * slot_bytes, 0x00020000);
+#pragma unroll
+            for (int s = 0; s < kLoads; s++) z.k[h][s] = __builtin_amdgcn_raw_buffer_load_b128(r, k_at[s], 0, kStream);
+            if constexpr (MX8) {
+              const rsrc_t e = __builtin_amdgcn_make_buffer_rsrc((void*)(ksp + (z.off[h] >> 5)), (short)0, z.rows[h] * slot_scales, 0x00020000);
+#pragma unroll
+              for (int s = 0; s < kLoads; s++) z.ke[h][s] = __builtin_amdgcn_raw_buffer_load_b8(e, k_at[s] >> 5, 0, 0);
+            }
+          } else {
+            const int64_t o = place_of[wave][it & 1][16 * h + c];
 #pragma unroll
             for (int s = 0; s < kLoads; s++) {
               const int d = MX8 ? 64 * s + 16 * g : 32 * s + 8 * g;
-              const int64_t e = o + (d < a.dim ? d : 0);
-              kw[h][s] = *reinterpret_cast<const u32x4*>(a.k + e * kSize);
-              if constexpr (MX8) ke[h][s] = a.ks[e >> 5];
+              const int64_t e = o + (d < dim ? d : 0);
+              z.k[h][s] = *reinterpret_cast<const u32x4*>(kp + e * kSize);
+              if constexpr (MX8) z.ke[h][s] = ksp[e >> 5];
             }
           }
         }
       };
       // V: kRow elements from kRow * c (+ 128 per run) of each of the eight keys; past dim: zeros or element
       // 0, whose output rows are not written
-      const auto load_v = [&](int it) {
-        const int t = min(first + it * kGrain, to - 1);
-        seen = 0u;
+      const auto load_v = [&](Tile& z, int it) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           rsrc_t rv, re;
           if constexpr (PAGED16) {
-            rv = __builtin_amdgcn_make_buffer_rsrc((void*)(a.v + off[h] * kSize), (short)0, rows[h] * slot_bytes, 0x00020000);
-            if constexpr (MX8) re = __builtin_amdgcn_make_buffer_rsrc((void*)(a.vs + (off[h] >> 5)), (short)0, rows[h] * slot_scales, 0x00020000);
+            rv = __builtin_amdgcn_make_buffer_rsrc((void*)(vp + z.off[h] * kSize), (short)0, z.rows[h] * slot_bytes, 0x00020000);
+            if constexpr (MX8) re = __builtin_amdgcn_make_buffer_rsrc((void*)(vsp + (z.off[h] >> 5)), (short)0, z.rows[h] * slot_scales, 0x00020000);
           }
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int j = 4 * h + i;
-            bool ok = false;
             int64_t o = 0;
-            if constexpr (!PAGED16) {
-              o = row_at(t, first + it * kGrain + 16 * h + 4 * g + i, ok);
-              seen |= ok ? 1u << j : 0u;
-            }
+            if constexpr (!PAGED16) o = place_of[wave][it & 1][16 * h + 4 * g + i];
 #pragma unroll
             for (int r = 0; r < kRuns; r++) {
               const int d = 128 * r + kRow * c;
-              const int64_t e = o + (d < a.dim ? d : 0);
-              if constexpr (PAGED16 && MX8) {
-                if constexpr (kRow == 8) vc[j][r] = __builtin_amdgcn_raw_buffer_load_b64(rv, v_at[i][r], 0, 0);
-                else vc[j][r] = (u32x2){__builtin_amdgcn_raw_buffer_load_b32(rv, v_at[i][r], 0, 0), 0u};
-                ve[j][r] = __builtin_amdgcn_raw_buffer_load_b8(re, v_at[i][r] >> 5, 0, 0);
-              } else if constexpr (PAGED16) {
-                if constexpr (kRow == 8) {
-                  vw[j][r] = __builtin_amdgcn_raw_buffer_load_b128(rv, v_at[i][r], 0, 0);
-                } else {
-                  const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(rv, v_at[i][r], 0, 0);
-                  vw[j][r] = (u32x4){w[0], w[1], 0u, 0u};
-                }
-              } else if constexpr (MX8) {
-                if constexpr (kRow == 8) vc[j][r] = *reinterpret_cast<const u32x2*>(a.v + e);
-                else vc[j][r] = (u32x2){*reinterpret_cast<const uint32_t*>(a.v + e), 0u};
-                ve[j][r] = a.vs[e >> 5];
-              } else if constexpr (kRow == 8) {
-                vw[j][r] = *reinterpret_cast<const u32x4*>(a.v + 2 * e);
+              const int64_t e = o + (d < dim ? d : 0);
+              u32x4& w = z.v[j][r];
+              if constexpr (kSize * kRow == 16) {
+                if constexpr (PAGED16) w = __builtin_amdgcn_raw_buffer_load_b128(rv, v_at[i][r], 0, kStream);
+                else w = *reinterpret_cast<const u32x4*>(vp + e * kSize);
+              } else if constexpr (kSize * kRow == 8) {
+                u32x2 x;
+                if constexpr (PAGED16) x = __builtin_amdgcn_raw_buffer_load_b64(rv, v_at[i][r], 0, kStream);
+                else x = *reinterpret_cast<const u32x2*>(vp + e * kSize);
+                w = (u32x4){x[0], x[1], 0u, 0u};
               } else {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(a.v + 2 * e);
-                vw[j][r] = (u32x4){w[0], w[1], 0u, 0u};
+                uint32_t x;
+                if constexpr (PAGED16) x = __builtin_amdgcn_raw_buffer_load_b32(rv, v_at[i][r], 0, kStream);
+                else x = *reinterpret_cast<const uint32_t*>(vp + e);
+                w = (u32x4){x, 0u, 0u, 0u};
+              }
+              if constexpr (MX8) {
+                if constexpr (PAGED16) z.ve[j][r] = __builtin_amdgcn_raw_buffer_load_b8(re, v_at[i][r] >> 5, 0, 0);
+                else z.ve[j][r] = vsp[e >> 5];
               }
             }
           }
         }
       };
 
-      place_tile(0);
-      load_k(0);
-      load_v(0);
-      for (int it = 0; it < n_tiles; it++) {
+      const auto attend = [&](Tile& z, int it) {
         const int t = first + it * kGrain;
-        bool all_seen, head_masked = false;  // every key is attended; keys before lo have to be cleared in V
+        // whether every key is attended, which of this lane's are (bit j: key 16 (j / 4) + 4 g + j % 4), and
+        // whether V holds others
+        bool all_seen, clear_v;
+        uint32_t seen = 0xFFu;
         if constexpr (PAGED16) {
-          all_seen = rows[0] == 16 && rows[1] == 16 && t >= lo;
-          head_masked = t < lo;
-          seen_now = 0xFFu;
+          all_seen = z.rows[0] == 16 && z.rows[1] == 16 && t >= lo;
+          clear_v = t < lo;
           if (!all_seen) {
-            seen_now = 0u;
+            seen = 0u;
 #pragma unroll
             for (int j = 0; j < 8; j++) {
               const int i = 4 * g + j % 4;
-              seen_now |= i < rows[j / 4] && t + 16 * (j / 4) + i >= lo ? 1u << j : 0u;
+              seen |= i < z.rows[j / 4] && t + 16 * (j / 4) + i >= lo ? 1u << j : 0u;
             }
           }
         } else {
-          seen_now = seen;
-          all_seen = __all(seen == 0xFFu);
-          head_masked = !all_seen;
-          page_next = fetch_pages(first + (it + 1) * kGrain);
+          all_seen = z.mask == ~0u;
+          clear_v = !all_seen;
+          seen = (z.mask >> (4 * g) & 15u) | (z.mask >> (4 * g + 16) & 15u) << 4;
         }
 
         // S^T: keys 4 g + i of half h, head c.
@@ -453,32 +485,31 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
           for (int st = 0; st < kSteps; st++) {
             u32x4 w;
             if constexpr (MX8) {
-              const u32x4 p = kw[h][st / 2];
-              w = widen<T>(st % 2 ? (u32x2){p[2], p[3]} : (u32x2){p[0], p[1]}, ke[h][st / 2]);
+              const u32x4 p = z.k[h][st / 2];
+              w = widen<T>(st % 2 ? (u32x2){p[2], p[3]} : (u32x2){p[0], p[1]}, z.ke[h][st / 2]);
             } else {
-              w = kw[h][st];
+              w = z.k[h][st];
             }
             if constexpr (!PAGED16) {
-              if ((MX8 ? 64 * (st / 2) + 16 * g : 32 * st + 8 * g) >= a.dim) w = (u32x4){0u, 0u, 0u, 0u};
+              if ((MX8 ? 64 * (st / 2) + 16 * g : 32 * st + 8 * g) >= dim) w = (u32x4){0u, 0u, 0u, 0u};
             }
             s = Vec<T>::mfma(__builtin_bit_cast(x8, w), qf[st], s);
           }
 #pragma unroll
           for (int i = 0; i < 4; i++) x[4 * h + i] = s[i];
         }
-        page = page_next;
-        place_tile(it + 1);
-        load_k(it + 1);
-        if (a.softcap > 0.f) {
+        place_tile(z, it + 2);
+        load_k(z, it + 2);
+        if (softcap > 0.f) {
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[j] = a.softcap * kLog2e * tanhf(x[j] * a.scale / a.softcap);
+          for (int j = 0; j < 8; j++) x[j] = kLog2e * soft_cap(x[j] * score_scale, softcap);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[j] *= a.scale * kLog2e;
+          for (int j = 0; j < 8; j++) x[j] *= score_scale * kLog2e;
         }
         if (!all_seen) {
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[j] = seen_now >> j & 1u ? x[j] : -INFINITY;
+          for (int j = 0; j < 8; j++) x[j] = seen >> j & 1u ? x[j] : -INFINITY;
         }
         float top = x[0];
 #pragma unroll
@@ -506,13 +537,13 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
           u32x4 w[8];
 #pragma unroll
           for (int j = 0; j < 8; j++) {
-            if constexpr (MX8) w[j] = widen<T>(vc[j][r], ve[j][r]);
-            else w[j] = vw[j][r];
+            if constexpr (MX8) w[j] = widen<T>((u32x2){z.v[j][r][0], z.v[j][r][1]}, z.ve[j][r]);
+            else w[j] = z.v[j][r];
           }
-          if (head_masked) {  // p = 0 there, and 0 * NaN is NaN
+          if (clear_v) {  // p = 0 there, and 0 * NaN is NaN
 #pragma unroll
             for (int j = 0; j < 8; j++)
-              if (!(seen_now >> j & 1u)) w[j] = (u32x4){0u, 0u, 0u, 0u};
+              if (!(seen >> j & 1u)) w[j] = (u32x4){0u, 0u, 0u, 0u};
           }
 #pragma unroll
           for (int i = 0; i < kRow; i++) {
@@ -523,7 +554,20 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
             acc[kRow * r + i] = Vec<T>::mfma(__builtin_bit_cast(x8, f), p, acc[kRow * r + i]);
           }
         }
-        load_v(it + 1);
+        load_v(z, it + 2);
+      };
+
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        place_tile(tile[i], i);
+        load_k(tile[i], i);
+        load_v(tile[i], i);
+      }
+      for (int it = 0;; it += 2) {
+        attend(tile[0], it);
+        if (it + 1 >= n_tiles) break;
+        attend(tile[1], it + 1);
+        if (it + 2 >= n_tiles) break;
       }
     }
 
@@ -557,12 +601,15 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
       }
     }
 
+    Kernarg& z = *fresh(args);
+    const int quads = dim / 4;
+    const FastDiv quads_div = copy_of(z.quads_div);
     const auto finish = [&](int h, int d, f32x4 o, float sum) {
       const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-      store4<T>((T*)a.out + (int64_t)b * a.ot + (int64_t)(first_head + h) * a.oh + d, o * inv);
+      store4<T>((T*)z.out + (int64_t)b * z.ot + (int64_t)(first_head + h) * z.oh + d, o * inv);
     };
     const auto put_lse = [&](int h, float top, float sum) {
-      if (a.lse) a.lse[(int64_t)b * a.heads * a.group + first_head + h] = sum == 0.f ? -INFINITY : kLn2 * (top - kShift + __log2f(sum));
+      if (z.lse) z.lse[(int64_t)b * z.heads * z.group + first_head + h] = sum == 0.f ? -INFINITY : kLn2 * (top - kShift + __log2f(sum));
     };
     // a head's maximum and sum over the waves
     const auto merged = [&](int h, float& sum) -> float {
@@ -577,12 +624,13 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
     const bool whole = at.grain == 0 && stop == row.grains;
     // Partials, one for a share that begins within a unit and one for a unit that ends past the share:
     // [16][dim] outputs, then [16] {maximum, sum}.
-    const uint32_t rows_at = (uint32_t)(16 * a.dim * 4), slot_size = rows_at + 16 * 8;
+    const uint32_t rows_at = (uint32_t)(16 * dim * 4), slot_size = rows_at + 16 * 8;
     rsrc_t pr;
-    if (!whole) pr = __builtin_amdgcn_make_buffer_rsrc(a.partial, (short)0, (int)(2 * a.wgs * slot_size), 0x00020000);
+    if (!whole) pr = __builtin_amdgcn_make_buffer_rsrc(z.partial, (short)0, (int)(2 * z.wgs * slot_size), 0x00020000);
+    const int items = n_heads * quads;
     const uint32_t mine_at = (2 * blockIdx.x + (at.grain == 0 ? 1u : 0u)) * slot_size;
-    for (int i = threadIdx.x; i < n_heads * quads; i += kThreads) {
-      const int h = i / quads, d = 4 * (i - h * quads);
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+      const int h = (int)quads_div.div((uint32_t)i), d = 4 * (i - h * quads);
       f32x4 o = *reinterpret_cast<const f32x4*>(lds + h * kLd + d);
 #pragma unroll
       for (int w = 1; w < kHalf; w++) o += *reinterpret_cast<const f32x4*>(lds + (w * n_heads + h) * kLd + d);
@@ -592,7 +640,7 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
         finish(h, d, o, sum);
         if (d == 0) put_lse(h, top, sum);
       } else {
-        put4(pr, mine_at + (uint32_t)(h * a.dim + d) * 4u, o);
+        put4(pr, mine_at + 16u * i, o);
         if (d == 0) __builtin_amdgcn_raw_buffer_store_b64((u32x2){fbits(top), fbits(sum)}, pr, mine_at + rows_at + h * 8, 0, 17);
       }
     }
@@ -600,75 +648,90 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
     // Join: the workgroup that arrives last adds the unit's partials in their order, of more than kFan in two steps:
     // groups of kGroup, then the groups. Every wave waits for its stores to be acknowledged before the
     // barrier and the counter's increment, so the last one (which takes the counter back to 0) sees all.
-    // A partial's counter is its group's first one's.
+    // A partial's counter is its group's first one's. The code is kept short: its instructions come from
+    // memory, as each workgroup runs it once.
     if (!whole) {
-      const int64_t u0 = at.at + (int64_t)at.unit * row.grains;
-      const int first = (int)quotient((uint64_t)(u0 + kLeast + per - 1), (uint64_t)per) - 1;  // the unit's first workgroup
-      const int members = (int)quotient((uint64_t)(u0 + row.grains - kLeast), (uint64_t)per) - first + 1;
-      const auto slot_of = [&](int i) -> int { return 2 * (first + i) + (i == 0 ? 1 : 0); };
+      const uint32_t u0 = at.at + (uint32_t)(at.unit * row.grains);
+      const int first = uniform((int)((u0 + kLeast + per - 1) / per)) - 1;  // the unit's first workgroup
+      const int members = uniform((int)((u0 + row.grains - kLeast) / per)) - first + 1;
       const int groups = members <= kFan ? 1 : ceil_div(members, kGroup), group = groups == 1 ? 0 : ((int)blockIdx.x - first) / kGroup;
+      float* share = lds;                  // sums of a head's runs of partials, below
+      float* weight = lds + 4 * kThreads;  // [head][kFan]
+#pragma unroll 1
       for (int level = 0; level < 2; level++) {
-        // the partials start, start + step, ... of this step, and whether their sum is the result
+        // the n partials start, start + step, ... of this step, and whether their sum is the result
         const int start = level == 0 ? group * kGroup : 0, step = level == 0 ? 1 : kGroup;
         const int n = level == 1 ? groups : groups == 1 ? members : min(kGroup, members - start);
         const bool result = level == 1 || groups == 1;
+        const uint32_t head_slot = 2u * (first + start) + (start == 0 ? 1u : 0u);  // others: every second one after it
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
         __syncthreads();
         if (threadIdx.x == 0)
-          is_last = atomicInc(a.counters + (level == 1 ? 2 * a.wgs + first : slot_of(start)), (unsigned)(n - 1)) == (unsigned)(n - 1);
+          is_last = atomicInc(z.counters + (level == 1 ? 2 * z.wgs + first : head_slot), (unsigned)(n - 1)) == (unsigned)(n - 1);
         __syncthreads();
-        if (!is_last) break;
-        // Weights 2^(m_i - m) of every head and partial, and the sums, a wave to a head at a time.
-        float* share = lds;                    // sums of a head's runs of partials, below
-        float* weight = lds + 4 * kThreads;    // [head][kFan]
-        for (int h = wave; h < n_heads; h += kWaves) {
-          float cm[kFan / 64], cl[kFan / 64], top = -INFINITY;
+        if (!uniform(is_last)) break;
+        const uint32_t at0 = 2u * (first + start) * slot_size, stride = 2u * step * slot_size, extra = start == 0 ? slot_size : 0u;
+        // a descriptor that ends with the n-th partial: loads past it give 0
+        const rsrc_t jr = __builtin_amdgcn_make_buffer_rsrc(z.partial, (short)0, (int)(at0 + (n - 1) * stride + (n == 1 ? extra : 0u) + slot_size), 0x00020000);
+        // The first outputs are on their way while the weights are worked out. Where a unit has fewer output
+        // quads than threads, groups of threads take every n-th partial.
+        const int split = items < kThreads ? kThreads / items : 1;
+        const int part = split > 1 ? (int)threadIdx.x / items : 0;
+        f32x4 v[kDeep];
+        const auto request = [&](int i, int ch) {  // partials ch, ch + split, ... of output quad i
+          uint32_t off = part < split && i < items ? at0 + ch * stride + 16u * i : 2u * kFar;
+          v[0] = get4(jr, off + (ch == 0 ? extra : 0u));
 #pragma unroll
-          for (int i = 0; i < kFan / 64; i++) {
-            const int ch = lane + 64 * i;
-            cm[i] = -INFINITY, cl[i] = 0.f;
-            if (ch < n) {
-              const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                  pr, slot_of(start + ch * step) * slot_size + rows_at + h * 8, 0, 17));
-              const uint32_t w0 = w[0], w1 = w[1];
-              cm[i] = bitsf(w0), cl[i] = bitsf(w1);
-            }
-            top = fmaxf(top, cm[i]);
+          for (int u = 1; u < kDeep; u++) {
+            off += split * stride;
+            v[u] = get4(jr, part < split && i < items ? off : 2u * kFar);
           }
+        };
+        request((int)threadIdx.x - part * items, part);
+        // Weights 2^(m_i - m) of head c and every 4 kWaves-th partial, and the sums
+        constexpr int kParts = kFan / (4 * kWaves);
+        float cm[kParts], cl[kParts], top = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < kFan / 64; i++) {
-            const float w = __builtin_amdgcn_exp2f(cm[i] - finite_or_zero(top));
-            weight[h * kFan + lane + 64 * i] = lane + 64 * i < n ? w : 0.f;
-            sum += w * cl[i];
-          }
-#pragma unroll
-          for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
-          if (lane == 0) {
-            wave_l[0][h] = sum, wave_m[0][h] = top;
-            if (result) put_lse(h, top, sum);
-          }
+        for (int i = 0; i < kParts; i++) {
+          const int ch = 4 * wave + g + 4 * kWaves * i;
+          const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(jr, at0 + ch * stride + (ch == 0 ? extra : 0u) + rows_at + 8 * c, 0, 17));
+          const uint32_t w0 = w[0], w1 = w[1];
+          cm[i] = ch < n && c < n_heads ? bitsf(w0) : -INFINITY, cl[i] = ch < n && c < n_heads ? bitsf(w1) : 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < kParts; i++) top = fmaxf(top, cm[i]);
+        top = wave_max(top);
+        wave_m[wave][c] = top;
         __syncthreads();
-        // Where a unit has fewer output quads than threads, groups of threads take every n-th partial.
-        const int items = n_heads * quads, split = items < kThreads ? kThreads / items : 1;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) top = fmaxf(top, wave_m[w][c]);
+#pragma unroll
+        for (int i = 0; i < kParts; i++) {
+          const float w = __builtin_amdgcn_exp2f(cm[i] - finite_or_zero(top));
+          if (c < n_heads) weight[c * kFan + 4 * wave + g + 4 * kWaves * i] = w;
+          sum += w * cl[i];
+        }
+        sum = wave_sum(sum);
+        wave_l[wave][c] = sum;
+        __syncthreads();
+        const auto joined = [&](int h, float& sum) -> float {  // a head's maximum and sum over the partials
+          float top = wave_m[0][h];
+          sum = wave_l[0][h];
+#pragma unroll
+          for (int w = 1; w < kWaves; w++) top = fmaxf(top, wave_m[w][h]), sum += wave_l[w][h];
+          return top;
+        };
+#pragma unroll 1
         for (int i0 = 0; i0 < items; i0 += kThreads) {
-          const int part = split > 1 ? (int)threadIdx.x / items : 0, i = split > 1 ? (int)threadIdx.x - part * items : i0 + (int)threadIdx.x;
+          const int i = i0 + (int)threadIdx.x - part * items;
           const bool mine = part < split && i < items;
-          const int h = mine ? i / quads : 0, d = mine ? 4 * (i - h * quads) : 0;
+          const int h = mine ? (int)quads_div.div((uint32_t)i) : 0, d = mine ? 4 * (i - h * quads) : 0;
           f32x4 o = {0.f, 0.f, 0.f, 0.f};
-          if (mine) {
-            const uint32_t from_row = (uint32_t)(h * a.dim + d) * 4u;
-            for (int ch = part; ch < n; ch += kDeep * split) {
-              f32x4 v[kDeep];
+#pragma unroll 1
+          for (int ch = part; ch < n; ch += kDeep * split) {
+            if (i0 > 0 || ch != part) request(i, ch);
 #pragma unroll
-              for (int u = 0; u < kDeep; u++)
-                v[u] = get4(pr, ch + u * split < n ? slot_of(start + (ch + u * split) * step) * slot_size + from_row : (uint32_t)kFar * 2u);
-#pragma unroll
-              for (int u = 0; u < kDeep; u++) o += v[u] * weight[h * kFan + min(ch + u * split, kFan - 1)];
-            }
+            for (int u = 0; u < kDeep; u++) o += v[u] * weight[h * kFan + min(ch + u * split, kFan - 1)];
           }
           if (split > 1) {
             if (mine) *reinterpret_cast<f32x4*>(share + 4 * threadIdx.x) = o;
@@ -677,21 +740,25 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(Args a) {
               for (int p = 1; p < split; p++) o += *reinterpret_cast<const f32x4*>(share + 4 * (p * items + i));
           }
           if (mine && part == 0) {
-            if (result) finish(h, d, o, wave_l[0][h]);
-            else put4(pr, slot_of(start) * slot_size + (uint32_t)(h * a.dim + d) * 4u, o);
+            float sum;
+            const float top = joined(h, sum);
+            if (result) {
+              finish(h, d, o, sum);
+              if (d == 0) put_lse(h, top, sum);
+            } else {
+              put4(pr, head_slot * slot_size + 16u * i, o);
+              if (d == 0) __builtin_amdgcn_raw_buffer_store_b64((u32x2){fbits(top), fbits(sum)}, pr, head_slot * slot_size + rows_at + h * 8, 0, 17);
+            }
           }
         }
         if (result) break;
-        if (threadIdx.x < n_heads)
-          __builtin_amdgcn_raw_buffer_store_b64((u32x2){fbits(wave_m[0][threadIdx.x]), fbits(wave_l[0][threadIdx.x])}, pr,
-                                                slot_of(start) * slot_size + rows_at + threadIdx.x * 8, 0, 17);
       }
     }
     __syncthreads();  // the next unit's merge uses the same memory
 
     at.grain = 0;
     if (stop < row.grains) break;
-    if (++at.unit == units) at = Place{b + 1, 0, 0, at.at + (int64_t)row.grains * units};
+    if (++at.unit == units) at = Place{b + 1, 0, 0, at.at + (uint32_t)(row.grains * units)};
   }
 }
 
@@ -709,10 +776,11 @@ struct Plan {
   size_t counter_bytes, bytes;
 };
 
-// The lengths are known on the device only. The grid is one round of workgroups, as many as the CUs hold at
-// a time, or fewer where max_len bounds the grains.
+// The lengths are known on the device only. The grid is one round of workgroups: one to a CU, whose waves
+// have 128 KB on their way, or two where two tiles per wave are less than that (131072 x 8 x 128 fp16:
+// 92 us with one, 100 with two, which double the partials; 64 x 16384 x 8 x 128 E4M3: 372 and 360); fewer where
+// max_len bounds the grains.
 constexpr int kCUs = 256;
-int per_cu(int dim) { return dim <= 64 ? 4 : dim <= 128 ? 2 : 1; }
 
 Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int window) {
   Plan p = {};
@@ -721,8 +789,10 @@ Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
   // positions from a sequence's first tile: a window may start within it
   const int64_t span = window > 0 && (int64_t)window + kTile < max_len ? (int64_t)window + kTile : max_len;
   const int64_t grains = ceil_div(span, (int64_t)kGrain), wgs = ceil_div(p.units * grains, (int64_t)kLeast);
-  if (grains < 2 * kLeast) return p;
-  p.wgs = (int)(wgs < kCUs * per_cu(c->dim) ? wgs : kCUs * per_cu(c->dim));
+  if (grains < 2 * kLeast || p.units * grains >= (int64_t)1 << 30) return p;  // (the device counts in 32 bits)
+  const int row_bytes = (c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256) * (c->fmt == MX_E4M3 ? 1 : 2);
+  const int most = kCUs * (2 * kGrain * 2 * row_bytes < 131072 ? 2 : 1);
+  p.wgs = (int)(wgs < most ? wgs : most);
   const size_t counters = (size_t)(p.units > 3 * p.wgs ? p.units : 3 * p.wgs);
   p.counter_bytes = ceil_div(counters * 4, (size_t)256) * 256;
   p.bytes = p.counter_bytes + (size_t)(2 * p.wgs) * 16 * (c->dim + 2) * 4;
@@ -787,9 +857,13 @@ extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads*
   }
   a.page_stride = cache->page_stride, a.head_stride = kv_head_stride(cache), a.slot_stride = slot_stride(cache);
   a.seqs = table->seqs, a.heads = cache->heads, a.group = q->heads / cache->heads, a.tiles = p.tiles, a.dim = cache->dim;
-  a.pages = cache->pages, a.page_size = cache->page_size, a.max_len = max_len, a.window = opts->window;
+  a.pages = cache->pages, a.page_size = cache->page_size, a.max_len = max_len, a.max_keys = (int)std::min<int64_t>((int64_t)table->cols * cache->page_size, INT32_MAX);
+  a.window = opts->window;
   a.scale = opts->scale, a.softcap = opts->softcap;
   a.page_div = FastDiv((uint32_t)cache->page_size);
+  a.units_div = FastDiv((uint32_t)(cache->heads * p.tiles));
+  a.wgs_div = FastDiv((uint32_t)(a.split ? p.wgs : 1));
+  a.quads_div = FastDiv((uint32_t)cache->dim / 4);
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
   const dim3 grid((unsigned)(a.split ? p.wgs : p.units));
