@@ -253,36 +253,23 @@ def mxrope_freqs_host(rot_dim: int, base: float, rule: int = MXROPE_PLAIN, param
     return list(freq), factor.value
 
 
-def _heads(t) -> _Heads:
-    """A [tokens][heads][dim] tensor; dim must be contiguous."""
-    tokens, heads, dim = t.shape
-    st, sh, sd = t.stride()
-    if sd != 1 and dim > 1:
-        raise MXError(MX_ERR_SHAPE, "mx_heads")
-    return _Heads(t.data_ptr(), heads, st, sh)
+_marshal = None
+
+
+def _load():
+    """The module that turns tensors into descriptors for the calls below (csrc/marshal.cpp); it needs torch."""
+    global _marshal
+    import torch  # noqa: F401  (loads the libraries that the module is linked to)
+    from . import _marshal as m
+    _marshal = m
+    return m
 
 
 def mxrope_run(f: int, rope: Rope, x, out, positions, inverse: bool = False, stream=None) -> None:
     """x, out: [tokens][heads][dim] (out may be x); positions: int32 [tokens]."""
-    a, b = _heads(x), _heads(out)
-    if x.shape != out.shape:
-        raise MXError(MX_ERR_SHAPE, "mxrope_run")
-    _check(_lib.mxrope_run(f, rope.ref, x.shape[0], x.shape[2], ctypes.addressof(a), ctypes.addressof(b),
-                           _ints(positions, "mxrope_run", (x.shape[0],)), int(inverse), _stream(stream)), "mxrope_run")
-
-
-def _ints(t, where: str, shape):
-    """Address of a dense int32 tensor of this shape; None stays None."""
-    if t is None:
-        return None
-    if t.dtype != _int32() or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise MXError(MX_ERR_SHAPE, where)
-    return t.data_ptr()
-
-
-def _int32():
-    import torch
-    return torch.int32
+    s = (_marshal or _load()).rope(f, rope.ref, x, out, positions, inverse, None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxrope_run")
 
 
 class KVCache:
@@ -312,25 +299,14 @@ def kv_layers(caches):
     return arr
 
 
-def _table(t, where: str) -> _Table:
-    seqs, cols = t.shape
-    return _Table(_ints(t, where, t.shape), seqs, cols)
-
-
 def mxkv_append_run(cache: KVCache, f: int, k, v, positions, table, seq=None, rope: Rope | None = None, q=None, q_out=None,
                     stream=None) -> None:
     """k, v: [tokens][heads][dim]; positions, seq: int32 [tokens]; table: int32 [seqs][cols]; q, q_out:
     [tokens][q heads][dim], turned in the same launch."""
-    where, n, dim = "mxkv_append_run", k.shape[0], cache.c.dim
-    for t in (k, v, q, q_out):
-        if t is not None and (t.shape[0] != n or t.shape[2] != dim):
-            raise MXError(MX_ERR_SHAPE, where)
-    hk, hv, tab = _heads(k), _heads(v), _table(table, where)
-    hq, ho = (None if t is None else _heads(t) for t in (q, q_out))
-    _check(_lib.mxkv_append_run(cache.ref, f, n, ctypes.addressof(hk), ctypes.addressof(hv), _ints(positions, where, (n,)),
-                                _ints(seq, where, (n,)), ctypes.addressof(tab), rope.ref if rope else None,
-                                ctypes.addressof(hq) if hq else None, ctypes.addressof(ho) if ho else None,
-                                _stream(stream)), where)
+    s = (_marshal or _load()).append(cache.ref, f, k, v, positions, table, seq, rope.ref if rope else None, q, q_out,
+                                     None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxkv_append_run")
 
 
 def mxattn_decode_workspace_size(cache: KVCache, seqs: int, q_heads: int, max_len: int, window: int = 0) -> int:
@@ -341,23 +317,18 @@ def mxattn_decode_run(cache: KVCache, f: int, q, out, table, lengths, max_len: i
                       window: int = 0, softcap: float = 0.0, workspace=None, workspace_bytes=None, stream=None) -> None:
     """q, out: [seqs][q heads][dim]; table: int32 [seqs][cols]; lengths, starts: int32 [seqs]; lse: fp32
     [seqs][q heads]; workspace: a zero-filled device buffer (a tensor's own size when workspace_bytes is omitted)."""
-    where, n = "mxattn_decode_run", q.shape[0]
-    if q.shape != out.shape or q.shape[2] != cache.c.dim or table.shape[0] != n or \
-            (lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous())):
-        raise MXError(MX_ERR_SHAPE, where)
-    if workspace is not None and workspace_bytes is None:
-        workspace_bytes = workspace.numel() * workspace.element_size()
-    hq, ho, tab, opts = _heads(q), _heads(out), _table(table, where), _AttnOpts(scale, softcap, window)
-    _check(_lib.mxattn_decode_run(cache.ref, f, ctypes.addressof(hq), ctypes.addressof(ho), _ptr(lse), ctypes.addressof(tab),
-                                  _ints(lengths, where, (n,)), _ints(starts, where, (n,)), max_len, ctypes.addressof(opts),
-                                  _ptr(workspace), int(workspace_bytes or 0), _stream(stream)), where)
+    s = (_marshal or _load()).attention(cache.ref, f, q, out, table, lengths, max_len, scale, lse, starts, window, softcap,
+                                        workspace, workspace_bytes, None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxattn_decode_run")
 
 
 def mxkv_copy_run(caches, pairs, stream=None) -> None:
     """caches: a list of KVCache, or kv_layers of it; pairs: int32 [n][2] of (source, destination) pages."""
     arr = caches if isinstance(caches, ctypes.Array) else kv_layers(caches)
-    _check(_lib.mxkv_copy_run(ctypes.addressof(arr), arr.count, _ints(pairs, "mxkv_copy_run", (pairs.shape[0], 2)),
-                              pairs.shape[0], _stream(stream)), "mxkv_copy_run")
+    s = (_marshal or _load()).copy(ctypes.addressof(arr), arr.count, pairs, None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxkv_copy_run")
 
 
 class KVPool:

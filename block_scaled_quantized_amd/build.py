@@ -2,7 +2,8 @@
 
 Every source is compiled for gfx950 only, with packed-fp32 instructions disabled
 (``-Xclang -target-feature -Xclang -packed-fp32-ops``). Objects go to ``_build/``; the shared
-library lands next to this file. ``python -m block_scaled_quantized_amd.build`` runs it.
+library lands next to this file, and beside it the Python binding's marshalling module (host code, against
+torch's headers). ``python -m block_scaled_quantized_amd.build`` runs it.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmxgemm.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "host_codec.cpp", "codec.hip", "mxgemm.hip", "mxgemm_ring.hip", "matvec.hip",
@@ -43,9 +45,37 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _marshal() -> str:
+    """Compile csrc/marshal.cpp (torch's Tensor accessors, no GPU code)."""
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "marshal.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", f"-isystem{home}/include", f"-isystem{home}/include/torch/csrc/api/include",
+           f"-isystem{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for marshal.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_marshal(obj: str) -> None:
+    """The module finds libmxgemm.so beside itself; torch's libraries are those the process has loaded."""
+    import torch
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, f"-L{HERE}", "-lmxgemm", "-Wl,-rpath,$ORIGIN",
+           f"-L{os.path.dirname(torch.__file__)}/lib", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the marshalling module failed:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
+        marshal = ex.submit(_marshal)
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
@@ -60,6 +90,7 @@ def build(verbose: bool = False) -> str:
     except OSError as e:
         raise RuntimeError(f"built library does not load: {e}") from e
     os.replace(tmp, LIB)
+    _link_marshal(marshal.result())
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -1,0 +1,208 @@
+// marshal.cpp -- the Python binding's calls of a decode step, whose kernels take a few microseconds:
+// tensors become the C entry points' descriptors here, by their C++ accessors. Through ctypes the descriptors of
+// one attention call took 10 us to fill, more than its kernel runs for a short sequence. Argument
+// marshalling only, as in api.py, which wraps these functions: each returns the library's status.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
+
+#include "mxgemm.h"
+
+namespace {
+
+struct TypeError : std::exception {
+  const char* what() const noexcept override { return "a torch tensor was expected"; }
+};
+struct PythonError : std::exception {};  // already set
+
+const at::Tensor& tensor(PyObject* o) {
+  if (!THPVariable_Check(o)) throw TypeError();
+  return THPVariable_Unpack(o);
+}
+
+int64_t integer(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PythonError();
+  return v;
+}
+
+int narrow(PyObject* o) {  // to int, as ctypes converts: the low 32 bits
+  return (int)integer(o);
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PythonError();
+  return v;
+}
+
+template <typename T>
+T* address(PyObject* o) {  // of a structure that the caller keeps; None: NULL
+  return o == Py_None ? nullptr : reinterpret_cast<T*>((uintptr_t)integer(o));
+}
+
+// A [tokens][heads][dim] tensor, dim contiguous. False: another shape.
+bool heads(const at::Tensor& t, mx_heads* h) {
+  if (t.dim() != 3 || (t.stride(2) != 1 && t.size(2) > 1)) return false;
+  *h = mx_heads{t.data_ptr(), (int)t.size(1), t.stride(0), t.stride(1)};
+  return true;
+}
+
+// The address of a dense int32 tensor of this shape; None: NULL.
+bool ints(PyObject* o, at::IntArrayRef shape, const int32_t** p) {
+  *p = nullptr;
+  if (o == Py_None) return true;
+  const at::Tensor& t = tensor(o);
+  if (t.scalar_type() != at::kInt || t.sizes() != shape || !t.is_contiguous()) return false;
+  *p = static_cast<const int32_t*>(t.data_ptr());
+  return true;
+}
+
+bool table_of(PyObject* o, mxkv_table* table) {
+  const at::Tensor& t = tensor(o);
+  if (t.dim() != 2 || t.scalar_type() != at::kInt || !t.is_contiguous()) return false;
+  *table = mxkv_table{static_cast<const int32_t*>(t.data_ptr()), (int)t.size(0), (int)t.size(1)};
+  return true;
+}
+
+void* stream_of(PyObject* o) {  // None: torch's current stream
+  if (o != Py_None) return address<void>(o);
+  static PyObject* current = nullptr;  // torch's own function of a device's current stream, kept for good
+  if (!current) {
+    PyObject* m = PyImport_ImportModule("torch._C");
+    current = m ? PyObject_GetAttrString(m, "_cuda_getCurrentRawStream") : nullptr;
+    Py_XDECREF(m);
+    if (!current) throw PythonError();
+  }
+  const c10::impl::VirtualGuardImpl gpu(c10::DeviceType::CUDA);
+  PyObject* device = PyLong_FromLong(gpu.getDevice().index());
+  PyObject* handle = device ? PyObject_CallOneArg(current, device) : nullptr;
+  Py_XDECREF(device);
+  if (!handle) throw PythonError();
+  void* stream = PyLong_AsVoidPtr(handle);
+  Py_DECREF(handle);
+  if (PyErr_Occurred()) throw PythonError();
+  return stream;
+}
+
+template <typename F>
+int unlocked(F call) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int status = call();
+  PyEval_RestoreThread(state);
+  return status;
+}
+
+// (f, rope, x, out, positions, inverse, stream)
+int rope(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[2]), &out = tensor(a[3]);
+  mx_heads hx, ho;
+  const int32_t* positions;
+  if (!heads(x, &hx) || !heads(out, &ho) || x.sizes() != out.sizes() || !ints(a[4], x.sizes().slice(0, 1), &positions)) return MX_ERR_SHAPE;
+  const int f = narrow(a[0]), tokens = (int)x.size(0), dim = (int)x.size(2), inverse = narrow(a[5]);
+  const mxrope* r = address<mxrope>(a[1]);
+  void* stream = stream_of(a[6]);
+  return unlocked([&] { return mxrope_run(f, r, tokens, dim, &hx, &ho, positions, inverse, stream); });
+}
+
+// (cache, f, k, v, positions, table, seq, rope, q, q_out, stream)
+int append(PyObject* const* a) {
+  const mxkv_cache* cache = address<mxkv_cache>(a[0]);
+  mx_heads h[4];
+  bool given[4];
+  const int64_t n = tensor(a[2]).dim() == 3 ? tensor(a[2]).size(0) : -1;
+  const int place[4] = {2, 3, 8, 9};
+  for (int i = 0; i < 4; i++) {
+    given[i] = i < 2 || a[place[i]] != Py_None;
+    if (!given[i]) continue;
+    const at::Tensor& t = tensor(a[place[i]]);
+    if (!heads(t, &h[i]) || t.size(0) != n || t.size(2) != cache->dim) return MX_ERR_SHAPE;
+  }
+  const int32_t *positions, *seq;
+  mxkv_table table;
+  if (!table_of(a[5], &table) || !ints(a[4], {n}, &positions) || !ints(a[6], {n}, &seq)) return MX_ERR_SHAPE;
+  const int f = narrow(a[1]);
+  const mxrope* r = address<mxrope>(a[7]);
+  void* stream = stream_of(a[10]);
+  return unlocked([&] {
+    return mxkv_append_run(cache, f, (int)n, &h[0], &h[1], positions, seq, &table, r, given[2] ? &h[2] : nullptr, given[3] ? &h[3] : nullptr, stream);
+  });
+}
+
+// (cache, f, q, out, table, lengths, max_len, scale, lse, starts, window, softcap, workspace, workspace_bytes, stream)
+int attention(PyObject* const* a) {
+  const mxkv_cache* cache = address<mxkv_cache>(a[0]);
+  const at::Tensor &q = tensor(a[2]), &out = tensor(a[3]);
+  mx_heads hq, ho;
+  mxkv_table table;
+  if (!heads(q, &hq) || !heads(out, &ho) || q.sizes() != out.sizes() || q.size(2) != cache->dim) return MX_ERR_SHAPE;
+  const int64_t n = q.size(0);
+  const int32_t *lengths, *starts;
+  if (!table_of(a[4], &table) || table.seqs != n || !ints(a[5], {n}, &lengths) || !ints(a[9], {n}, &starts)) return MX_ERR_SHAPE;
+  float* lse = nullptr;
+  if (a[8] != Py_None) {
+    const at::Tensor& t = tensor(a[8]);
+    if (t.sizes() != q.sizes().slice(0, 2) || !t.is_contiguous() || t.scalar_type() != at::kFloat) return MX_ERR_SHAPE;
+    lse = static_cast<float*>(t.data_ptr());
+  }
+  void* workspace = nullptr;
+  size_t bytes = 0;
+  if (THPVariable_Check(a[12])) {
+    const at::Tensor& t = tensor(a[12]);
+    workspace = t.data_ptr(), bytes = t.nbytes();
+  } else {
+    workspace = address<void>(a[12]);
+  }
+  if (a[13] != Py_None) bytes = (size_t)integer(a[13]);
+  const int f = narrow(a[1]), max_len = narrow(a[6]);
+  const mxattn_opts opts = {(float)number(a[7]), (float)number(a[11]), narrow(a[10])};
+  void* stream = stream_of(a[14]);
+  return unlocked([&] {
+    return mxattn_decode_run(cache, f, &hq, &ho, lse, &table, lengths, starts, max_len, &opts, workspace, bytes, stream);
+  });
+}
+
+// (layers, n_layers, pairs, stream)
+int copy(PyObject* const* a) {
+  const mxkv_cache* layers = address<mxkv_cache>(a[0]);
+  const at::Tensor& t = tensor(a[2]);
+  const int32_t* pairs;
+  if (t.dim() != 2 || !ints(a[2], {t.size(0), 2}, &pairs)) return MX_ERR_SHAPE;
+  const int n_layers = narrow(a[1]), n = (int)t.size(0);
+  void* stream = stream_of(a[3]);
+  return unlocked([&] { return mxkv_copy_run(layers, n_layers, pairs, n, stream); });
+}
+
+template <int (*F)(PyObject* const*), int COUNT>
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  if (count != COUNT) {
+    PyErr_Format(PyExc_TypeError, "%d arguments were expected", COUNT);
+    return nullptr;
+  }
+  try {
+    return PyLong_FromLong(F(args));
+  } catch (const TypeError& e) {
+    PyErr_SetString(PyExc_TypeError, e.what());
+  } catch (const PythonError&) {
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+template <int (*F)(PyObject* const*), int COUNT>
+constexpr PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<F, COUNT>)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef methods[] = {method<rope, 7>("rope"), method<append, 11>("append"), method<attention, 15>("attention"), method<copy, 4>("copy"),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__marshal() { return PyModule_Create(&module); }
