@@ -9,6 +9,7 @@
 // lose the phase of far positions altogether; after the reduction to half a turn an fp32 sine and
 // cosine are exact to 2 ulp.
 #include <cmath>
+#include <type_traits>
 
 #include "kvcache.h"
 #include "quant_rules.h"
@@ -18,7 +19,6 @@ using namespace mx;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;      // rows that a thread loads before it uses the first
 constexpr int kMaxTrig = 512;  // (token, pair) angles of a workgroup
 constexpr int kStage = 8192;   // 16-bit elements of rotated keys that a workgroup stages
 
@@ -28,9 +28,40 @@ struct Unit {  // 16 bytes of elements
   T e[N];
 };
 
+// What is written is not read by this launch: stored non-temporally, it leaves the caches to the rows that are
+// read (4096 x 32 x 128 bf16: 14.4 -> 12.4 us). Reads gain by it (STREAM) where a call's rows exceed what the
+// caches can hold from the kernel that made them, and lose below (201 MB: 43 -> 38 us; 26 MB: 6.9 -> 8.5); the
+// reads from memory also want four rows of a thread on their way where two do for the caches (38 against
+// 41 us; 12.4 against 11.9).
+constexpr int64_t kStreamBytes = 128 << 20;
+constexpr int batch_of(bool stream) { return stream ? 4 : 2; }  // rows that a thread loads before it uses the first
+template <bool STREAM, typename T>
+MX_DEV Unit<T> load_unit(const T* p) {
+  const u32x4* q = reinterpret_cast<const u32x4*>(p);
+  if constexpr (STREAM) return __builtin_bit_cast(Unit<T>, __builtin_nontemporal_load(q));
+  else return __builtin_bit_cast(Unit<T>, *q);
+}
+template <typename T>
+MX_DEV void store_unit(T* p, const Unit<T>& v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
+}
+
 MX_DEV float to_f32(_Float16 x) { return (float)x; }
 MX_DEV float to_f32(__bf16 x) { return (float)x; }
 MX_DEV float to_f32(float x) { return x; }
+
+// A pair (a, b) turned, w = (cos, sin). One product is rounded, the other is not, and the sum is rounded to fp32
+// before it is to T: the same steps in every kernel, so that the append writes the bits that mxrope_run
+// does. (For binary16 a barrier keeps the compiler from its mixed fma, which rounds once.)
+template <typename T>
+MX_DEV T round_to(float x) {
+  if constexpr (std::is_same<T, _Float16>::value) asm("" : "+v"(x));
+  return (T)x;
+}
+template <typename T>
+MX_DEV T turn_a(float a, float b, float2 w) { return round_to<T>(__builtin_fmaf(a, w.x, -(b * w.y))); }
+template <typename T>
+MX_DEV T turn_b(float a, float b, float2 w) { return round_to<T>(__builtin_fmaf(b, w.x, a * w.y)); }
 
 struct Rotation {
   const double* freq;
@@ -59,9 +90,10 @@ struct Split {
 
 // A workgroup's rows: tokens t0 .. t0 + tokens - 1 times heads h0 .. h0 + heads - 1. store(token, head,
 // element, values, count) takes a unit or single elements. COPY_TAIL: whether copied elements need a store.
-template <typename T, bool PAIRS, bool VEC, typename Store>
+template <typename T, bool PAIRS, bool VEC, bool STREAM, typename Store>
 MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, int t0, int tokens, const T* __restrict__ x,
                         int64_t xt, int64_t xh, int h0, int heads, Split sp, bool copy_tail, float2* trig, Store store) {
+  constexpr int kBatch = batch_of(STREAM);
   constexpr int U = Unit<T>::N;
   const int per = kThreads / sp.items;  // rows of one pass
   const int item = threadIdx.x % sp.items, r0 = threadIdx.x / sp.items;
@@ -82,8 +114,8 @@ MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, in
       if (mine && row < rows) {
         const T* p = x + (int64_t)(t0 + tok[u]) * xt + (int64_t)(h0 + head[u]) * xh + a;
         if constexpr (VEC) {
-          lo[u] = *reinterpret_cast<const Unit<T>*>(p);
-          if (!PAIRS && turns) hi[u] = *reinterpret_cast<const Unit<T>*>(p + half);
+          lo[u] = load_unit<STREAM>(p);
+          if (!PAIRS && turns) hi[u] = load_unit<STREAM>(p + half);
         } else {
           lo[u].e[0] = p[0];
           if (turns) hi[u].e[0] = p[PAIRS ? 1 : half];
@@ -105,16 +137,16 @@ MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, in
           for (int i = 0; i < U / 2; i++) {
             const float p = to_f32(lo[u].e[2 * i]), q = to_f32(lo[u].e[2 * i + 1]);
             const float2 w = cs[i];
-            lo[u].e[2 * i] = (T)(p * w.x - q * w.y);
-            lo[u].e[2 * i + 1] = (T)(q * w.x + p * w.y);
+            lo[u].e[2 * i] = turn_a<T>(p, q, w);
+            lo[u].e[2 * i + 1] = turn_b<T>(p, q, w);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < (VEC ? U : 1); i++) {
             const float p = to_f32(lo[u].e[i]), q = to_f32(hi[u].e[i]);
             const float2 w = cs[i];
-            lo[u].e[i] = (T)(p * w.x - q * w.y);
-            hi[u].e[i] = (T)(q * w.x + p * w.y);
+            lo[u].e[i] = turn_a<T>(p, q, w);
+            hi[u].e[i] = turn_b<T>(p, q, w);
           }
         }
       }
@@ -138,23 +170,26 @@ struct RopeArgs {
   int64_t xt, xh, ot, oh;
   int tokens, heads, tile_t, tile_h, groups;  // groups: runs of tile_h heads
   Split split;
+  bool stream;
 };
 
-template <typename T, bool PAIRS, bool VEC>
+template <typename T, bool PAIRS, bool VEC, bool STREAM>
 MX_DEV void rope_block(const RopeArgs& a, int block, float2* trig) {
   const int g = block % a.groups, t0 = (block / a.groups) * a.tile_t, h0 = g * a.tile_h;
   T* out = (T*)a.out;
-  rotate_rows<T, PAIRS, VEC>(a.rot, a.pos, t0, min(a.tile_t, a.tokens - t0), (const T*)a.x, a.xt, a.xh, h0,
+  rotate_rows<T, PAIRS, VEC, STREAM>(a.rot, a.pos, t0, min(a.tile_t, a.tokens - t0), (const T*)a.x, a.xt, a.xh, h0,
                              min(a.tile_h, a.heads - h0), a.split, a.x != a.out, trig,
                              [&](int t, int h, int e, const Unit<T>& v) {
-                               put<T, VEC>(out + (int64_t)(t0 + t) * a.ot + (int64_t)(h0 + h) * a.oh + e, v);
+                               T* p = out + (int64_t)(t0 + t) * a.ot + (int64_t)(h0 + h) * a.oh + e;
+                               if constexpr (VEC) store_unit(p, v);
+                               else p[0] = v.e[0];
                              });
 }
 
-template <typename T, bool PAIRS, bool VEC>
+template <typename T, bool PAIRS, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   __shared__ float2 trig[kMaxTrig];
-  rope_block<T, PAIRS, VEC>(a, blockIdx.x, trig);
+  rope_block<T, PAIRS, VEC, STREAM>(a, blockIdx.x, trig);
 }
 
 // ---- append ---------------------------------------------------------------------------------
@@ -193,7 +228,7 @@ MX_DEV void fill_slots(const AppendArgs& a, int t0, int tokens, int64_t* slot) {
 template <typename T>
 MX_DEV void write_unit(const Unit<T>& v, bool mx8, uint8_t* codes, uint8_t* scales, int64_t at) {
   if (!mx8) {
-    if (at >= 0) *reinterpret_cast<Unit<T>*>(codes + 2 * at) = v;
+    if (at >= 0) store_unit(reinterpret_cast<T*>(codes + 2 * at), v);
     return;
   }
   // Four neighbouring lanes hold a block of 32: they agree on its scale, and each writes its 8 codes.
@@ -227,14 +262,14 @@ MX_DEV void write_unit(const Unit<T>& v, bool mx8, uint8_t* codes, uint8_t* scal
   if (at % 32 == 0) scales[at / 32] = (uint8_t)E;
 }
 
-template <typename T, bool PAIRS, bool VEC>
+template <typename T, bool PAIRS, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8) {
   __shared__ float2 trig[kMaxTrig];
   __shared__ T stage[kStage];
   __shared__ int64_t slot[kMaxTrig];
   int block = blockIdx.x;
   if (block < a.q_blocks) {
-    rope_block<T, PAIRS, VEC>(a.q, block, trig);
+    rope_block<T, PAIRS, VEC, STREAM>(a.q, block, trig);
     return;
   }
   block -= a.q_blocks;
@@ -244,7 +279,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8
   const int tokens = min(a.k.tile_t, a.k.tokens - t0), heads = min(a.k.tile_h, a.k.heads - h0);
   fill_slots(a, t0, tokens, slot);
   if (key && a.turn)
-    rotate_rows<T, PAIRS, VEC>(a.k.rot, a.k.pos, t0, tokens, (const T*)a.k.x, a.k.xt, a.k.xh, h0, heads, a.k.split, true, trig,
+    rotate_rows<T, PAIRS, VEC, STREAM>(a.k.rot, a.k.pos, t0, tokens, (const T*)a.k.x, a.k.xt, a.k.xh, h0, heads, a.k.split, true, trig,
                                [&](int t, int h, int e, const Unit<T>& v) {
                                  put<T, VEC>(stage + (t * heads + h) * a.dim + e, v);
                                });
@@ -262,7 +297,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8
     Unit<T> v = {};
     if (mine)
       v = key && a.turn ? *reinterpret_cast<const Unit<T>*>(stage + row * a.dim + 8 * unit)
-                        : *reinterpret_cast<const Unit<T>*>(x + (int64_t)(t0 + t) * xt + (int64_t)(h0 + h) * xh + 8 * unit);
+                        : load_unit<false>(x + (int64_t)(t0 + t) * xt + (int64_t)(h0 + h) * xh + 8 * unit);
     const int64_t s = mine ? slot[t] : -1;
     write_unit<T>(v, mx8, codes, scales, s < 0 ? -1 : s + (h0 + h) * a.head_stride + 8 * unit);
   }
@@ -289,7 +324,7 @@ void tile(RopeArgs& a, int max_rows) {
   const int per = kThreads / a.split.items;  // rows of a pass
   const int half = a.rot.half > 0 ? a.rot.half : 1;
   a.tile_h = a.heads < max_rows ? a.heads : max_rows;
-  const int cap = max_rows < per * kBatch ? max_rows : per * kBatch;  // one batch of loads per thread
+  const int cap = max_rows < per * batch_of(a.stream) ? max_rows : per * batch_of(a.stream);  // one batch of loads per thread
   a.tile_t = 1;
   while (2 * a.tile_t * a.tile_h <= cap && 2 * a.tile_t * half <= kMaxTrig && (a.tokens + a.tile_t - 1) / a.tile_t > 1024)
     a.tile_t *= 2;
@@ -321,20 +356,26 @@ RopeArgs rope_args(const mxrope* r, int tokens, int dim, const mx_heads* x, cons
 
 template <typename T>
 void rope_launch(const RopeArgs& a, bool pairs, bool vec, dim3 grid, hipStream_t st) {
+  const bool stream = vec && a.stream;
   const dim3 block(kThreads);
-  if (pairs && vec) hipLaunchKernelGGL((rope_kernel<T, true, true>), grid, block, 0, st, a);
-  else if (pairs) hipLaunchKernelGGL((rope_kernel<T, true, false>), grid, block, 0, st, a);
-  else if (vec) hipLaunchKernelGGL((rope_kernel<T, false, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((rope_kernel<T, false, false>), grid, block, 0, st, a);
+  if (pairs && stream) hipLaunchKernelGGL((rope_kernel<T, true, true, true>), grid, block, 0, st, a);
+  else if (pairs && vec) hipLaunchKernelGGL((rope_kernel<T, true, true, false>), grid, block, 0, st, a);
+  else if (pairs) hipLaunchKernelGGL((rope_kernel<T, true, false, false>), grid, block, 0, st, a);
+  else if (stream) hipLaunchKernelGGL((rope_kernel<T, false, true, true>), grid, block, 0, st, a);
+  else if (vec) hipLaunchKernelGGL((rope_kernel<T, false, true, false>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((rope_kernel<T, false, false, false>), grid, block, 0, st, a);
 }
 
 template <typename T>
 void append_launch(const AppendArgs& a, bool pairs, bool vec, bool mx8, dim3 grid, hipStream_t st) {
+  const bool stream = vec && a.k.stream;
   const dim3 block(kThreads);
-  if (pairs && vec) hipLaunchKernelGGL((append_kernel<T, true, true>), grid, block, 0, st, a, mx8);
-  else if (pairs) hipLaunchKernelGGL((append_kernel<T, true, false>), grid, block, 0, st, a, mx8);
-  else if (vec) hipLaunchKernelGGL((append_kernel<T, false, true>), grid, block, 0, st, a, mx8);
-  else hipLaunchKernelGGL((append_kernel<T, false, false>), grid, block, 0, st, a, mx8);
+  if (pairs && stream) hipLaunchKernelGGL((append_kernel<T, true, true, true>), grid, block, 0, st, a, mx8);
+  else if (pairs && vec) hipLaunchKernelGGL((append_kernel<T, true, true, false>), grid, block, 0, st, a, mx8);
+  else if (pairs) hipLaunchKernelGGL((append_kernel<T, true, false, false>), grid, block, 0, st, a, mx8);
+  else if (stream) hipLaunchKernelGGL((append_kernel<T, false, true, true>), grid, block, 0, st, a, mx8);
+  else if (vec) hipLaunchKernelGGL((append_kernel<T, false, true, false>), grid, block, 0, st, a, mx8);
+  else hipLaunchKernelGGL((append_kernel<T, false, false, false>), grid, block, 0, st, a, mx8);
 }
 
 }  // namespace
@@ -387,6 +428,7 @@ extern "C" int mxrope_run(int f, const mxrope* rope, int tokens, int dim, const 
   if (x->data == out->data && (x->token_stride != out->token_stride || x->head_stride != out->head_stride)) return MX_ERR_SHAPE;
   const bool pairs = rope->layout == MXROPE_PAIRS, vec = vec_ok(rope->layout, rope->rot_dim, 16 / bytes);
   RopeArgs a = rope_args(rope, tokens, dim, x, out, positions, inverse, 16 / bytes, vec);
+  a.stream = 2ll * tokens * x->heads * dim * bytes >= kStreamBytes;
   tile(a, 1 << 20);
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
@@ -425,10 +467,12 @@ extern "C" int mxkv_append_run(const mxkv_cache* cache, int f, int tokens, const
   const bool pairs = rope && rope->layout == MXROPE_PAIRS, vec = !rope || vec_ok(rope->layout, rope->rot_dim, 8);
   AppendArgs a = {};
   a.k = rope_args(rope, tokens, cache->dim, k, nullptr, positions, 0, 8, vec);
+  a.k.stream = 4ll * tokens * (cache->heads * 2 + (q ? q->heads : 0)) * cache->dim >= kStreamBytes;
   tile(a.k, kStage / cache->dim);
   int64_t q_blocks = 0;
   if (q) {
     a.q = rope_args(rope, tokens, cache->dim, q, q_out, positions, 0, 8, vec);
+    a.q.stream = a.k.stream;
     tile(a.q, 1 << 20);
     q_blocks = blocks_of(a.q);
   }
