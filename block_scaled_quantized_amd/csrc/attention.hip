@@ -176,9 +176,11 @@ struct Place {
 };
 
 // No unit is cut within this many grains of its ends, for shares of `per` grains: a cut costs two partials
-// and their join, about as much as four grains, so larger shares leave small units whole (78 x 16 units of
-// two grains: 17 us against 24 with cuts anywhere; 8 units of four, all there is: 11.5 us against 12.8).
-MX_DEV int least_of(uint32_t per) { return (int)min(max((per + 1u) / 3u, 1u), 4u); }
+// and their join, about as much as four grains, so larger shares leave small units whole (8 x 8 units of 6 to
+// 368 grains, per = 4: 22.5 us with 2, 25.4 with 1; 12 x 5 units of 11 grains, per = 2: 14.5 us with 1, 15.8
+// with 2). Units of fewer than kCut are not cut (8 units of four grains: 10.7 us, in four workgroups each 11.9).
+constexpr int kCut = 5;
+MX_DEV int least_of(uint32_t per, int grains) { return grains < kCut ? grains : (int)min(max(per / 2u, 1u), 4u); }
 
 // This workgroup's share of the grains, from..to, of equal size (which is returned) but for the cuts'
 // distance from the units' ends. Every wave sums up the lengths by itself, four neighbouring sequences to a
@@ -189,11 +191,18 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
   const int lane = threadIdx.x & 63;
   uint32_t n[kEach], own, before, total;
   const auto look = [&](int b0) {
+    int length[kEach], start[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {  // all loads before the first use
+      const int b = min(b0 + kEach * lane + i, a.seqs - 1);
+      length[i] = a.lengths[b];
+      start[i] = a.starts ? a.starts[b] : 0;
+    }
     own = 0u;
 #pragma unroll
     for (int i = 0; i < kEach; i++) {
-      const int b = b0 + kEach * lane + i;
-      n[i] = b < a.seqs ? (uint32_t)row_of(a, b).grains : 0u;
+      const uint32_t grains = (uint32_t)row_of(a, length[i], start[i]).grains;
+      n[i] = b0 + kEach * lane + i < a.seqs ? grains : 0u;
       own += n[i];
     }
     before = wave_scan(own);
@@ -208,7 +217,6 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
   }
   all *= (uint32_t)units;  // below 2^31
   const uint32_t per = copy_of(a.wgs_div).div(all + (uint32_t)a.wgs - 1u);
-  const int least = least_of(per);
   uint32_t sum = 0u;
   from = to = Place{a.seqs, 0, 0, all};
   for (int b0 = 0; b0 < a.seqs; b0 += kLook) {
@@ -233,6 +241,7 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
       Place p = {b, 0, 0, (sum + start) * units};
       p.unit = uniform((int)((cut - p.at) / size));
       p.grain = (int)(cut - p.at - p.unit * size);
+      const int least = least_of(per, (int)size);
       if (p.grain < least) p.grain = 0;
       else if ((int)size - p.grain < least) p.grain = 0, p.unit++;
       if (p.unit == units) p = Place{b + 1, 0, 0, p.at + size * units};
@@ -250,13 +259,19 @@ MX_DEV float soft_cap(float s, float c) {
   return c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
+// Tiles of a wave on their way: two, or one of D = 256, whose registers would not hold a second.
+constexpr int tiles_ahead(int D) { return D == 256 ? 1 : 2; }
+// Of D = 256, 16-bit rows take more than 256 registers (16 x 8192 x 4 fp16: 88 us, spilled into 256 of them 101;
+// E4M3 fits: 64 us against 69).
+constexpr int waves_per_simd(int D, bool mx8) { return D == 256 && !mx8 ? 1 : 2; }
+
 // D: 64, 128 or 256, the head size rounded up. T: type of q, out and the arithmetic. MX8: E4M3 cache.
 // PAGED16: page_size % 16 == 0, so that the 16 keys of half a tile lie in one page: their place is a
 // buffer descriptor in scalar registers, whose size also turns keys past the end, missing pages and
 // elements past dim into zeros. For other page sizes a lane works out one key's place and the others
 // read it from LDS.
 template <int D, typename T, bool MX8, bool PAGED16>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args) {
+__global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kernel(Args) {
   typedef typename Vec<T>::x8 x8;
   constexpr float kShift = Vec<T>::kShift;
   constexpr int kSteps = D / 32;          // matrix instructions of one score tile
@@ -265,10 +280,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
   constexpr int kRow = D == 64 ? 4 : 8;
   constexpr int kOut = D / 16;            // accumulators
   constexpr int kSize = MX8 ? 1 : 2;      // bytes of an element
+  constexpr int kAhead = tiles_ahead(D);
   constexpr int kBlock = 32;              // tiles of a wave whose pages it looks up at a time
   extern __shared__ float lds[];          // merge: [kWaves / 2][head][D + kPad]; join: sums, then [head][kFan] weights
-  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
+  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16], head_m[16], head_l[16];
   __shared__ int is_last;
+  constexpr bool kQueryInLds = D == 256;  // its 32 registers would be spilled: a wave's lanes keep them here
+  __shared__ u32x4 query_of[kQueryInLds ? kWaves : 1][kQueryInLds ? kSteps : 1][64];
   __shared__ int64_t place_of[PAGED16 ? 1 : kWaves][2][kTile];  // of the keys of a wave's two tiles
 
   Kernarg* const args = (Kernarg*)__builtin_amdgcn_kernarg_segment_ptr();
@@ -296,14 +314,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
     const float score_scale = a.scale, softcap = a.softcap;
 
     // Query fragments: column c, the elements that this lane's K loads hold.
-    x8 qf[kSteps];
+    x8 qf[kQueryInLds ? 1 : kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; s++) {
       const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
       u32x4 w = {0u, 0u, 0u, 0u};
       if (c < n_heads && d < dim)
         w = *reinterpret_cast<const u32x4*>((const T*)a.q + (int64_t)b * a.qt + (int64_t)(first_head + c) * a.qh + d);
-      qf[s] = __builtin_bit_cast(x8, w);
+      if constexpr (kQueryInLds) query_of[wave][s][lane] = w;
+      else qf[s] = __builtin_bit_cast(x8, w);
     }
 
     // The page of a key, -1 where there is none. A page number is read before the length that says whether the
@@ -343,15 +362,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
     for (int i = 0; i < kOut; i++) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
 
-    // Two tiles are on their way: a tile's K is loaded again as soon as its scores are formed, its V
-    // as soon as it is added up.
+    // A tile's K is loaded again as soon as its scores are formed, its V as soon as it is added up.
     struct Tile {
       u32x4 k[2][kLoads], v[8][kRuns];
       uint32_t ke[2][kLoads], ve[8][kRuns];
       int64_t off[2];        // PAGED16: element offset of each half's page slot, and its keys
       int rows[2];
       uint32_t mask;         // not PAGED16: bit i: key i is attended
-    } tile[2];
+    } tile[kAhead];
     for (int first = from + wave * kTile; first < to; first += kBlock * kGrain) {
       const int upto = min(to, first + kBlock * kGrain);  // the tiles of this block end here
       const int n_tiles = (upto - first + kGrain - 1) / kGrain;
@@ -482,12 +500,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
         }
 
         // S^T: keys 4 g + i of half h, head c.
-        float x[8];
+        f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        for (int st = 0; st < kSteps; st++) {
+          x8 q;
+          if constexpr (kQueryInLds) q = __builtin_bit_cast(x8, query_of[wave][st][lane]);
+          else q = qf[st];
 #pragma unroll
-          for (int st = 0; st < kSteps; st++) {
+          for (int h = 0; h < 2; h++) {
             u32x4 w;
             if constexpr (MX8) {
               const u32x4 p = z.k[h][st / 2];
@@ -498,13 +518,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
             if constexpr (!PAGED16) {
               if ((MX8 ? 64 * (st / 2) + 16 * g : 32 * st + 8 * g) >= dim) w = (u32x4){0u, 0u, 0u, 0u};
             }
-            s = Vec<T>::mfma(__builtin_bit_cast(x8, w), qf[st], s);
+            s[h] = Vec<T>::mfma(__builtin_bit_cast(x8, w), q, s[h]);
           }
-#pragma unroll
-          for (int i = 0; i < 4; i++) x[4 * h + i] = s[i];
         }
-        place_tile(z, it + 2);
-        load_k(z, it + 2);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] = s[j / 4][j % 4];
+        place_tile(z, it + kAhead);
+        load_k(z, it + kAhead);
         if (softcap > 0.f) {
 #pragma unroll
           for (int j = 0; j < 8; j++) x[j] = kLog2e * soft_cap(x[j] * score_scale, softcap);
@@ -539,6 +560,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
         // out^T += V^T P^T
 #pragma unroll
         for (int r = 0; r < kRuns; r++) {
+          if constexpr (kRuns > 1) __builtin_amdgcn_sched_barrier(0);  // one run's values at a time: else they spill
           u32x4 w[8];
 #pragma unroll
           for (int j = 0; j < 8; j++) {
@@ -559,20 +581,24 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
             acc[kRow * r + i] = Vec<T>::mfma(__builtin_bit_cast(x8, f), p, acc[kRow * r + i]);
           }
         }
-        load_v(z, it + 2);
+        load_v(z, it + kAhead);
       };
 
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
+      for (int i = 0; i < kAhead; i++) {
         place_tile(tile[i], i);
         load_k(tile[i], i);
         load_v(tile[i], i);
       }
-      for (int it = 0;; it += 2) {
-        attend(tile[0], it);
-        if (it + 1 >= n_tiles) break;
-        attend(tile[1], it + 1);
-        if (it + 2 >= n_tiles) break;
+      if constexpr (kAhead == 1) {
+        for (int it = 0; it < n_tiles; it++) attend(tile[0], it);
+      } else {
+        for (int it = 0;; it += 2) {
+          attend(tile[0], it);
+          if (it + 1 >= n_tiles) break;
+          attend(tile[1], it + 1);
+          if (it + 2 >= n_tiles) break;
+        }
       }
     }
 
@@ -583,9 +609,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
     __syncthreads();
     constexpr int kLd = D + kPad, kHalf = kWaves / 2;
     {
-      float top = wave_m[0][c];
+      float top = wave_m[0][c], sum = 0.f;
 #pragma unroll
       for (int w = 1; w < kWaves; w++) top = fmaxf(top, wave_m[w][c]);
+#pragma unroll
+      for (int w = 0; w < kWaves; w++) sum += wave_l[w][c] * __builtin_amdgcn_exp2f(wave_m[w][c] - finite_or_zero(top));
+      if (wave == 0) head_m[c] = top, head_l[c] = sum;
       const float f = __builtin_amdgcn_exp2f(m - finite_or_zero(top));
       float* o = lds + ((wave % kHalf) * n_heads + c) * kLd;
 #pragma unroll
@@ -616,16 +645,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
     const auto put_lse = [&](int h, float top, float sum) {
       if (z.lse) z.lse[(int64_t)b * z.heads * z.group + first_head + h] = sum == 0.f ? -INFINITY : kLn2 * (top - kShift + __log2f(sum));
     };
-    // a head's maximum and sum over the waves
-    const auto merged = [&](int h, float& sum) -> float {
-      float top = wave_m[0][h];
-#pragma unroll
-      for (int w = 1; w < kWaves; w++) top = fmaxf(top, wave_m[w][h]);
-      sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; w++) sum += wave_l[w][h] * __builtin_amdgcn_exp2f(wave_m[w][h] - finite_or_zero(top));
-      return top;
-    };
     const bool whole = at.grain == 0 && stop == row.grains;
     // Partials, one for a share that begins within a unit and one for a unit that ends past the share:
     // [16][dim] outputs, then [16] {maximum, sum}.
@@ -639,8 +658,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
       f32x4 o = *reinterpret_cast<const f32x4*>(lds + h * kLd + d);
 #pragma unroll
       for (int w = 1; w < kHalf; w++) o += *reinterpret_cast<const f32x4*>(lds + (w * n_heads + h) * kLd + d);
-      float sum;
-      const float top = merged(h, sum);
+      const float sum = head_l[h], top = head_m[h];
       if (whole) {
         finish(h, d, o, sum);
         if (d == 0) put_lse(h, top, sum);
@@ -656,7 +674,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void decode_kernel(Args
     // A partial's counter is its group's first one's. The code is kept short: its instructions come from
     // memory, as each workgroup runs it once.
     if (!whole) {
-      const uint32_t u0 = at.at + (uint32_t)(at.unit * row.grains), least = least_of(per);
+      const uint32_t u0 = at.at + (uint32_t)(at.unit * row.grains), least = least_of(per, row.grains);
       const int first = uniform((int)((u0 + least + per - 1) / per)) - 1;  // the unit's first workgroup
       const int members = uniform((int)((u0 + row.grains - least) / per)) - first + 1;
       const int groups = members <= kFan ? 1 : ceil_div(members, kGroup), group = groups == 1 ? 0 : ((int)blockIdx.x - first) / kGroup;
@@ -794,9 +812,9 @@ Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
   // positions from a sequence's first tile: a window may start within it
   const int64_t span = window > 0 && (int64_t)window + kTile < max_len ? (int64_t)window + kTile : max_len;
   const int64_t grains = ceil_div(span, (int64_t)kGrain), wgs = p.units * grains;
-  if (grains < 2 || p.units * grains >= (int64_t)1 << 30) return p;  // (the device counts in 32 bits)
-  const int row_bytes = (c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256) * (c->fmt == MX_E4M3 ? 1 : 2);
-  const int most = kCUs * (2 * kGrain * 2 * row_bytes < 131072 ? 2 : 1);
+  if (grains < kCut || p.units * grains >= (int64_t)1 << 30) return p;  // (the device counts in 32 bits)
+  const int D = c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256;
+  const int most = kCUs * (tiles_ahead(D) * kGrain * 2 * D * (c->fmt == MX_E4M3 ? 1 : 2) < 131072 ? 2 : 1);
   p.wgs = (int)(wgs < most ? wgs : most);
   const size_t counters = (size_t)(p.units > 3 * p.wgs ? p.units : 3 * p.wgs);
   p.counter_bytes = ceil_div(counters * 4, (size_t)256) * 256;
