@@ -55,7 +55,7 @@ struct Args {
   int seqs, heads, group, tiles, dim, cols, pages, page_size, max_len, max_keys, window, wgs;
   bool split;
   float scale, softcap;
-  FastDiv page_div, units_div, wgs_div, quads_div;  // units: of one sequence
+  FastDiv page_div, units_div, tiles_div, wgs_div, quads_div;  // units: of one sequence
 };
 
 template <typename T>
@@ -153,7 +153,6 @@ MX_DEV Row row_of(Kernarg& a, int length, int start) {
   r.grains = max(1, (r.hi - r.base + kGrain - 1) / kGrain);
   return r;
 }
-MX_DEV Row row_of(Kernarg& a, int b) { return row_of(a, a.lengths[b], a.starts ? a.starts[b] : 0); }
 
 MX_DEV int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
@@ -190,18 +189,18 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
   constexpr int kEach = 4, kLook = 64 * kEach;
   const int lane = threadIdx.x & 63;
   uint32_t n[kEach], own, before, total;
+  const int32_t *lengths = a.lengths, *starts = a.starts ? a.starts : lengths;
   const auto look = [&](int b0) {
-    int length[kEach], start[kEach];
+    int length[kEach], start[kEach];  // all loads before the first use
 #pragma unroll
-    for (int i = 0; i < kEach; i++) {  // all loads before the first use
+    for (int i = 0; i < kEach; i++) {
       const int b = min(b0 + kEach * lane + i, a.seqs - 1);
-      length[i] = a.lengths[b];
-      start[i] = a.starts ? a.starts[b] : 0;
+      length[i] = lengths[b], start[i] = starts[b];
     }
     own = 0u;
 #pragma unroll
     for (int i = 0; i < kEach; i++) {
-      const uint32_t grains = (uint32_t)row_of(a, length[i], start[i]).grains;
+      const uint32_t grains = (uint32_t)row_of(a, length[i], a.starts ? start[i] : 0).grains;
       n[i] = b0 + kEach * lane + i < a.seqs ? grains : 0u;
       own += n[i];
     }
@@ -305,7 +304,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
   while (at.b < end.b || (at.b == end.b && (at.unit < end.unit || (at.unit == end.unit && at.grain < end.grain)))) {
     Kernarg& a = *fresh(args);
     const int b = at.b, dim = a.dim;
-    const int ht = at.unit % a.tiles, hk = at.unit / a.tiles;
+    const int hk = (int)copy_of(a.tiles_div).div((uint32_t)at.unit), ht = at.unit - hk * a.tiles;
     const int first_head = hk * a.group + 16 * ht, n_heads = min(16, a.group - 16 * ht);
     const int64_t head_at = (int64_t)hk * a.head_stride, page_stride = a.page_stride, slot_stride = a.slot_stride;
     const int32_t* table = a.table + (int64_t)b * a.cols;
@@ -313,29 +312,35 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
     const int page_size = a.page_size, pages = a.pages, cols = a.cols;
     const float score_scale = a.scale, softcap = a.softcap;
 
-    // Query fragments: column c, the elements that this lane's K loads hold.
-    x8 qf[kQueryInLds ? 1 : kSteps];
-#pragma unroll
-    for (int s = 0; s < kSteps; s++) {
-      const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
-      u32x4 w = {0u, 0u, 0u, 0u};
-      if (c < n_heads && d < dim)
-        w = *reinterpret_cast<const u32x4*>((const T*)a.q + (int64_t)b * a.qt + (int64_t)(first_head + c) * a.qh + d);
-      if constexpr (kQueryInLds) query_of[wave][s][lane] = w;
-      else qf[s] = __builtin_bit_cast(x8, w);
-    }
-
-    // The page of a key, -1 where there is none. A page number is read before the length that says whether the
-    // key counts has come, so that the two loads wait together.
-    const auto page_at = [&](int index) -> int {
-      const int p = table[min(index, cols - 1)];
-      return p >= 0 && p < pages ? p : -1;
-    };
+    // The unit's first loads wait together: its row's length, the pages that the wave's first keys have if the row
+    // starts at 0 (a page's number is read before it is known that its keys count), and the queries.
     const bool from_zero = !a.starts && a.window == 0;
     const int ahead = at.grain * kGrain + wave * kTile;  // the wave's first key, if the row starts at 0
+    const auto page_at = [&](int key) -> int { return table[min((int)page_div.div((uint32_t)key), cols - 1)]; };
+    const auto page_or_none = [&](int p) -> int { return p >= 0 && p < pages ? p : -1; };
     int page_ahead = -1;
-    if (from_zero) page_ahead = page_at((int)page_div.div((uint32_t)(ahead + (PAGED16 ? (lane >> 1) * kGrain + (lane & 1) * 16 : lane & (kTile - 1)))));
-    Row row = row_of(a, b);
+    const int length = a.lengths[b], start = (a.starts ? a.starts : a.lengths)[b];
+    if (from_zero) page_ahead = page_at(ahead + (PAGED16 ? (lane >> 1) * kGrain + (lane & 1) * 16 : lane & (kTile - 1)));
+
+    // Query fragments: column c, the elements that this lane's K loads hold; zeros past the heads and past dim.
+    x8 qf[kQueryInLds ? 1 : kSteps];
+    {
+      const T* q = (const T*)a.q + (int64_t)b * a.qt + (int64_t)(first_head + (c < n_heads ? c : 0)) * a.qh;
+      u32x4 w[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; s++) {
+        const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+        w[s] = *reinterpret_cast<const u32x4*>(q + (d < dim ? d : 0));
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; s++) {
+        const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+        if (c >= n_heads || d >= dim) w[s] = (u32x4){0u, 0u, 0u, 0u};
+        if constexpr (kQueryInLds) query_of[wave][s][lane] = w[s];
+        else qf[s] = __builtin_bit_cast(x8, w[s]);
+      }
+    }
+    Row row = row_of(a, length, a.starts ? start : 0);
     row = Row{uniform(row.lo), uniform(row.hi), from_zero ? 0 : uniform(row.base), uniform(row.grains)};
     const int stop = b == end.b && at.unit == end.unit ? end.grain : row.grains;
     const int from = row.base + at.grain * kGrain, to = min(row.hi, row.base + stop * kGrain), lo = row.lo;
@@ -379,15 +384,17 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
       // else: lane i % 32 holds the page of key i of the next tile to be placed
       int page = -1;
       const auto fetch_page = [&](int it) -> int {
-        return page_at((int)page_div.div((uint32_t)min(first + it * kGrain + (lane & (kTile - 1)), to)));
+        return page_or_none(page_at(min(first + it * kGrain + (lane & (kTile - 1)), to)));
       };
       if constexpr (PAGED16) {
         const int key = first + (lane >> 1) * kGrain + (lane & 1) * 16, i = (int)page_div.div((uint32_t)key);
-        const int p = from_zero && first == ahead ? page_ahead : page_at(i);
+        int p = page_ahead;
+        if (!from_zero || first != ahead) p = page_at(key);
+        p = page_or_none(p);
         const int64_t off = p * page_stride + (key - i * page_size) * slot_stride + head_at;
         off_lo = (int)off, off_hi = p < 0 ? -1 : (int)(off >> 32);
       } else {
-        page = from_zero && first == ahead ? page_ahead : fetch_page(0);
+        page = from_zero && first == ahead ? page_or_none(page_ahead) : fetch_page(0);
       }
 
       const auto place_tile = [&](Tile& z, int it) {
@@ -885,6 +892,7 @@ extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads*
   a.scale = opts->scale, a.softcap = opts->softcap;
   a.page_div = FastDiv((uint32_t)cache->page_size);
   a.units_div = FastDiv((uint32_t)(cache->heads * p.tiles));
+  a.tiles_div = FastDiv((uint32_t)p.tiles);
   a.wgs_div = FastDiv((uint32_t)(a.split ? p.wgs : 1));
   a.quads_div = FastDiv((uint32_t)cache->dim / 4);
   if (int s = check_arch()) return s;
