@@ -261,8 +261,9 @@ MX_DEV float soft_cap(float s, float c) {
 // Tiles of a wave on their way: two, or one of D = 256, whose registers would not hold a second.
 constexpr int tiles_ahead(int D) { return D == 256 ? 1 : 2; }
 // Of D = 256, 16-bit rows take more than 256 registers (16 x 8192 x 4 fp16: 88 us, spilled into 256 of them 101;
-// E4M3 fits: 64 us against 69).
-constexpr int waves_per_simd(int D, bool mx8) { return D == 256 && !mx8 ? 1 : 2; }
+// E4M3 fits: 64 us against 69). D = 64 fits three waves (78 x 16 short rows E4M3: 17 us, 20 with two, 24 spilled
+// into four).
+constexpr int waves_per_simd(int D, bool mx8) { return D == 256 && !mx8 ? 1 : D == 64 ? 3 : 2; }
 
 // D: 64, 128 or 256, the head size rounded up. T: type of q, out and the arithmetic. MX8: E4M3 cache.
 // PAGED16: page_size % 16 == 0, so that the 16 keys of half a tile lie in one page: their place is a
