@@ -6,7 +6,7 @@
 // share it), so everything else serves its loads: 16 query heads of one cache head are the columns of a
 // 16x16x32 matrix instruction (columns without a head idle: the matrix cores have more than ten times
 // the rate that the memory asks of them), K and V go from global memory to registers with no LDS
-// between, and the lengths are split over workgroups.
+// between, two tiles ahead, and all sequences' keys are shared evenly among one round of workgroups.
 //
 // A wave takes tiles of 32 keys, as two halves of 16. Scores are formed transposed, S^T = K Q^T (rows:
 // keys, columns: heads): lane (c = lane % 16, g = lane / 16) loads 16 bytes of key row c. It then
@@ -18,6 +18,12 @@
 //
 // E4M3 elements become 16-bit ones on the way by gfx950's scaled conversion, which takes the block's
 // power of two: a lane's 8 K elements and its V elements of one key lie in one block of 32.
+//
+// Measured (reads of a large array by a row maximum: 6.4 TB/s): 64 x 16384 keys x 8 x 128 E4M3, 2.2 GB, 359 us,
+// 6.2 TB/s; 131072 keys x 8 x 128 fp16, 537 MB, 92 us, 5.8 TB/s; the same bytes over 16 x 8192 keys x 4 x
+// 256, 88 us. Where a call's work is a few grains per workgroup, its time is the chain of dependent memory
+// latencies (lengths and pages, keys, and for cut units partials, counter, partials) and the instructions that come from
+// memory: 6 us for rows of a few keys, 10.6 us for 8 x 500 keys of 128.
 #include <algorithm>
 
 #include "kvcache.h"
@@ -35,7 +41,7 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kTile = 32;                // keys of a wave's tile
 constexpr int kGrain = kTile * kWaves;   // keys that the workgroup's waves take in turn: the unit of work
 constexpr int kFan = 128, kGroup = 64;   // partials that one workgroup joins; groups of more
-constexpr int kDeep = 16;                // partials that a joining thread has on their way
+constexpr int kDeep = 8;                 // partials that a joining thread has on their way
 constexpr int kPad = 4;                  // floats that keep the heads' rows of the merge on different banks
 // Keys and values are read once: marked non-temporal, they leave the L2 to the program, whose prologue and
 // joins otherwise wait for their instructions (131072 x 8 x 128 fp16: 114 -> 103 us).
@@ -177,40 +183,30 @@ struct Place {
 // No unit is cut within this many grains of its ends, for shares of `per` grains: a cut costs two partials
 // and their join, about as much as four grains, so larger shares leave small units whole (8 x 8 units of 6 to
 // 368 grains, per = 4: 22.5 us with 2, 25.4 with 1; 12 x 5 units of 11 grains, per = 2: 14.5 us with 1, 15.8
-// with 2). Units of fewer than kCut are not cut (8 units of four grains: 10.7 us, in four workgroups each 11.9).
+// with 2). Units of fewer than kCut are not cut (8 units of four grains: 10.6 us, in four workgroups each 11.9;
+// of five: 14.0 whole, 12.0 cut).
 constexpr int kCut = 5;
 MX_DEV int least_of(uint32_t per, int grains) { return grains < kCut ? grains : (int)min(max(per / 2u, 1u), 4u); }
 
 // This workgroup's share of the grains, from..to, of equal size (which is returned) but for the cuts'
-// distance from the units' ends. Every wave sums up the lengths by itself, four neighbouring sequences to a
-// lane: a handful of loads that all find in the caches, where a launch that planned would cost its own
-// latency, and no barrier.
+// distance from the units' ends. Every wave sums up the lengths by itself, a sequence to a lane: a handful
+// of loads that all find in the caches, where a launch that planned would cost its own latency, and no
+// barrier. (Short code counts here: a workgroup runs it once, and its instructions come from memory.)
 MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
-  constexpr int kEach = 4, kLook = 64 * kEach;
   const int lane = threadIdx.x & 63;
-  uint32_t n[kEach], own, before, total;
+  uint32_t size, before, total;
   const int32_t *lengths = a.lengths, *starts = a.starts ? a.starts : lengths;
   const auto look = [&](int b0) {
-    int length[kEach], start[kEach];  // all loads before the first use
-#pragma unroll
-    for (int i = 0; i < kEach; i++) {
-      const int b = min(b0 + kEach * lane + i, a.seqs - 1);
-      length[i] = lengths[b], start[i] = starts[b];
-    }
-    own = 0u;
-#pragma unroll
-    for (int i = 0; i < kEach; i++) {
-      const uint32_t grains = (uint32_t)row_of(a, length[i], a.starts ? start[i] : 0).grains;
-      n[i] = b0 + kEach * lane + i < a.seqs ? grains : 0u;
-      own += n[i];
-    }
-    before = wave_scan(own);
+    const int b = min(b0 + lane, a.seqs - 1), length = lengths[b], start = starts[b];
+    size = (uint32_t)row_of(a, length, a.starts ? start : 0).grains;
+    if (b0 + lane >= a.seqs) size = 0u;
+    before = wave_scan(size);
     total = (uint32_t)__builtin_amdgcn_readlane((int)before, 63);
-    before -= own;
+    before -= size;
   };
   look(0);
   uint32_t all = total;
-  for (int b0 = kLook; b0 < a.seqs; b0 += kLook) {
+  for (int b0 = 64; b0 < a.seqs; b0 += 64) {
     look(b0);
     all += total;
   }
@@ -218,32 +214,22 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
   const uint32_t per = copy_of(a.wgs_div).div(all + (uint32_t)a.wgs - 1u);
   uint32_t sum = 0u;
   from = to = Place{a.seqs, 0, 0, all};
-  for (int b0 = 0; b0 < a.seqs; b0 += kLook) {
-    if (a.seqs > kLook) look(b0);
+  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+    if (a.seqs > 64) look(b0);
 #pragma unroll 1
     for (int side = 0; side < 2; side++) {
       const uint32_t cut = min(all, (blockIdx.x + side) * per);
       const uint32_t q = copy_of(a.units_div).div(cut) - sum;  // grains of a unit's column before the cut's
       if (cut >= all || q >= total) continue;  // (a cut before this block wraps around)
-      // the last lane that starts at or before q, and the sequence among its four
-      const int at_lane = 63 - __builtin_clzll(__ballot(before <= q));
-      uint32_t start = (uint32_t)__builtin_amdgcn_readlane((int)before, at_lane), size = 0u;
-      int b = b0 + kEach * at_lane;
-#pragma unroll
-      for (int i = 0; i < kEach; i++) {
-        const uint32_t next = (uint32_t)__builtin_amdgcn_readlane((int)n[i], at_lane);
-        if (i == 0 || q >= start + size) {
-          if (i) b++, start += size;
-          size = next;
-        }
-      }
-      Place p = {b, 0, 0, (sum + start) * units};
-      p.unit = uniform((int)((cut - p.at) / size));
-      p.grain = (int)(cut - p.at - p.unit * size);
-      const int least = least_of(per, (int)size);
+      const int at_lane = 63 - __builtin_clzll(__ballot(before <= q));  // the last one that starts at or before q
+      const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)size, at_lane);
+      Place p = {b0 + at_lane, 0, 0, (sum + (uint32_t)__builtin_amdgcn_readlane((int)before, at_lane)) * units};
+      p.unit = uniform((int)((cut - p.at) / n));
+      p.grain = (int)(cut - p.at - p.unit * n);
+      const int least = least_of(per, (int)n);
       if (p.grain < least) p.grain = 0;
-      else if ((int)size - p.grain < least) p.grain = 0, p.unit++;
-      if (p.unit == units) p = Place{b + 1, 0, 0, p.at + size * units};
+      else if ((int)n - p.grain < least) p.grain = 0, p.unit++;
+      if (p.unit == units) p = Place{p.b + 1, 0, 0, p.at + n * units};
       if (side) to = p;
       else from = p;
     }
@@ -804,7 +790,7 @@ size_t lds_bytes(int D, int n_heads, bool split) {
 struct Plan {
   int64_t units;
   int tiles, wgs;  // wgs: workgroups that share the grains; 0: no unit is worth splitting
-  size_t counter_bytes, bytes;
+  size_t bytes;
 };
 
 // The lengths are known on the device only. The grid is one round of workgroups: one to a CU, whose waves
@@ -812,6 +798,9 @@ struct Plan {
 // 92 us with one, 100 with two, which double the partials; 64 x 16384 x 8 x 128 E4M3: 372 and 360); fewer where
 // max_len bounds the grains.
 constexpr int kCUs = 256;
+// Three counters per workgroup, at one place for every call: a workspace that served another shape has its
+// partials past them.
+constexpr size_t kCounterBytes = 3 * 2 * kCUs * 4;
 
 Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int window) {
   Plan p = {};
@@ -824,9 +813,7 @@ Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
   const int D = c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256;
   const int most = kCUs * (tiles_ahead(D) * kGrain * 2 * D * (c->fmt == MX_E4M3 ? 1 : 2) < 131072 ? 2 : 1);
   p.wgs = (int)(wgs < most ? wgs : most);
-  const size_t counters = (size_t)(p.units > 3 * p.wgs ? p.units : 3 * p.wgs);
-  p.counter_bytes = ceil_div(counters * 4, (size_t)256) * 256;
-  p.bytes = p.counter_bytes + (size_t)(2 * p.wgs) * 16 * (c->dim + 2) * 4;
+  p.bytes = kCounterBytes + (size_t)(2 * p.wgs) * 16 * (c->dim + 2) * 4;
   return p;
 }
 
@@ -884,7 +871,7 @@ extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads*
   a.wgs = p.wgs;
   if (a.split) {
     a.counters = (uint32_t*)workspace;
-    a.partial = (float*)((uint8_t*)workspace + p.counter_bytes);
+    a.partial = (float*)((uint8_t*)workspace + kCounterBytes);
   }
   a.page_stride = cache->page_stride, a.head_stride = kv_head_stride(cache), a.slot_stride = slot_stride(cache);
   a.seqs = table->seqs, a.heads = cache->heads, a.group = q->heads / cache->heads, a.tiles = p.tiles, a.dim = cache->dim;

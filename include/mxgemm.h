@@ -406,11 +406,11 @@ typedef struct {
  *  - Scores, statistics and sums are fp32; the probabilities are rounded to 16 bits for the matrix
  *    cores. E4M3 elements are scaled into f's format (exact in bfloat16; in binary16 where the value
  *    is in its range, as every value that mxkv_append_run wrote from binary16 is).
- * Workspace, as for mxmatvec_run: the sequences' lengths are split over workgroups, whose partial
- * results and one counter per row of workgroups live in a caller-owned device buffer of
+ * Workspace, as for mxmatvec_run: the rows' keys are shared evenly among workgroups, and where a share
+ * cuts a row, partial results and counters live in a caller-owned device buffer of
  * mxattn_decode_workspace_size() bytes, zero-filled before its first use and left reusable by every
- * call. Calls that may overlap in time need separate workspaces. Without one, or with too small a one, a
- * sequence is not split (same results up to fp32 summation order; slow for long sequences). The
+ * call, of this or other shapes. Calls that may overlap in time need separate workspaces. Without one, or with too small a one, a
+ * row is not cut (same results up to fp32 summation order; slow for long rows). The
  * partials are joined in a fixed order: results are deterministic.
  * Rules (MX_ERR_SHAPE): q->heads a multiple of the cache's heads, out->heads == q->heads;
  * seqs * q->heads < 2^24; 1 <= max_len < 2^30; scale finite, softcap and window not negative. table->seqs is the batch

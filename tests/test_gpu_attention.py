@@ -308,3 +308,83 @@ def test_attention_streams_and_graph(monkeypatch):
         g.replay()
         torch.cuda.synchronize()
         assert np.array_equal(f64(o2), want) and np.array_equal(f64(o), want)
+
+
+@pytest.mark.parametrize("kind,cache,dim,page", [("f16", "f16", 64, 64), ("bf16", "e4m3", 64, 30), ("f16", "f16", 128, 16)])
+def test_attention_joins_many_parts(kind, cache, dim, page):
+    """One long row of one head, over every workgroup: its parts are joined in groups first. The same bits every time."""
+    api = require_gpu()
+    n = 100001
+    say(f"attention {cache}: {n} keys of one head of {dim}, pages of {page}")
+    pages = -(-n // page) + 1
+    c = Cache(cache, "heads", pages, page, 1, dim, 8)
+    table = tables([n], page, pages, 3)
+    q = normal((1, 5, dim), kind, 5)
+    ws = torch.zeros(api.mxattn_decode_workspace_size(c.c, 1, 5, n), dtype=torch.uint8, device="cuda")
+    outs = [run(api, c, kind, q, table, [n], n, ws=ws) for _ in range(3)]
+    check(c, kind, q, *outs[0], table, [n])
+    assert all(torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1]) for o, l in outs[1:])
+
+
+@pytest.mark.parametrize("window", [0, 700])
+def test_attention_many_ragged_rows(window):
+    """More rows than lanes, from none to thousands of keys: the shares' cuts fall anywhere."""
+    api = require_gpu()
+    g = np.random.Generator(np.random.PCG64(12))
+    lengths = [int(x) for x in np.exp(g.uniform(0, np.log(4000), 150))]
+    lengths[3] = lengths[70] = lengths[149] = 0
+    lengths[64] = 4000
+    starts = [int(x) for x in g.integers(0, 600, 150)]
+    say(f"attention: 150 ragged rows, window={window}")
+    pages = sum(-(-n // 32) for n in lengths)
+    c = Cache("f16", "slots", pages, 32, 2, 64, 9)
+    table = tables(lengths, 32, pages, 3)
+    q = normal((150, 4, 64), "f16", 5)
+    for s in (None, starts):
+        out, lse = run(api, c, "f16", q, table, lengths, 4000, starts=s, window=window)
+        check(c, "f16", q, out, lse, table, lengths, s, window)
+
+
+def test_attention_workspace_serves_other_shapes():
+    """One workspace, zero-filled once, for calls of different batches, heads and lengths in turn."""
+    api = require_gpu()
+    say("attention: one workspace for several shapes")
+    sets = []
+    for i, (cache, hq, hk, dim, lengths) in enumerate([("f16", 4, 2, 64, [5000]), ("f16", 16, 8, 128, [3000, 10, 900, 1500]),
+                                                       ("e4m3", 8, 1, 256, [2000] * 3), ("f16", 96, 12, 32, [700] * 9)]):
+        pages = sum(-(-n // 16) for n in lengths)
+        c = Cache(cache, "heads", pages, 16, hk, dim, i)
+        sets.append((c, normal((len(lengths), hq, dim), "f16", i), tables(lengths, 16, pages, i), lengths))
+    need = [api.mxattn_decode_workspace_size(c.c, q.shape[0], q.shape[1], max(n)) for c, q, _, n in sets]
+    assert min(need) > 0 and len(set(need)) > 1
+    ws = torch.zeros(max(need), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 1, 0, 3, 2, 0):
+        c, q, table, lengths = sets[i]
+        out, lse = run(api, c, "f16", q, table, lengths, max(lengths), ws=ws)
+        check(c, "f16", q, out, lse, table, lengths)
+
+
+def test_attention_large_bf16_values():
+    """Values near bfloat16's largest: the sums of a row stay in range."""
+    api = require_gpu()
+    say("attention: values of 2^100")
+    c = Cache("bf16", "heads", 64, 16, 1, 64, 4)
+    c.planes[1] *= 2.0 ** 100
+    c.v = c.v * 2.0 ** 100
+    table = tables([1000], 16, 64, 3)
+    q = normal((1, 4, 64), "bf16", 5)
+    for split in (True, False):
+        out, lse = run(api, c, "bf16", q, table, [1000], 1000, split=split)
+        check(c, "bf16", q, out, lse, table, [1000])
+
+
+def test_attention_empty_rows_among_many():
+    """A batch of empty rows only, with a workspace: zeros and -inf, and the counters stay at zero."""
+    api = require_gpu()
+    say("attention: empty rows")
+    c = Cache("f16", "heads", 40, 16, 2, 128, 4)
+    table = tables([0, 600, 0], 16, 40, 3, cols=60)
+    q = normal((3, 6, 128), "f16", 5)
+    for lengths in ([0, 0, 0], [0, 600, 0], [-1, 600, -2 ** 31]):
+        out, lse = run(api, c, "f16", q, table, lengths, 960)
+        check(c, "f16", q, out, lse, table, lengths)
