@@ -6,7 +6,7 @@
 // share it), so everything else serves its loads: 16 query heads of one cache head are the columns of a
 // 16x16x32 matrix instruction (columns without a head idle: the matrix cores have more than ten times
 // the rate that the memory asks of them), K and V go from global memory to registers with no LDS
-// between, two tiles ahead, and all sequences' keys are shared evenly among one round of workgroups.
+// between, up to two tiles ahead, and the keys of long rows are shared evenly among one round of workgroups.
 //
 // A wave takes tiles of 32 keys, as two halves of 16. Scores are formed transposed, S^T = K Q^T (rows:
 // keys, columns: heads): lane (c = lane % 16, g = lane / 16) loads 16 bytes of key row c. It then
@@ -23,7 +23,7 @@
 // 6.2 TB/s; 131072 keys x 8 x 128 fp16, 537 MB, 92 us, 5.8 TB/s; the same bytes over 16 x 8192 keys x 4 x
 // 256, 88 us. Where a call's work is a few grains per workgroup, its time is the chain of dependent memory
 // latencies (lengths and pages, keys, and for cut units partials, counter, partials) and the instructions that come from
-// memory: 6 us for rows of a few keys, 10.6 us for 8 x 500 keys of 128.
+// memory: 5.3 us for rows of a few keys, 9.4 us for 8 x 500 keys of 128 (a kernel of one store: 3.6 us).
 #include <algorithm>
 
 #include "kvcache.h"
@@ -59,7 +59,6 @@ struct Args {
   float* partial;
   int64_t qt, qh, ot, oh, page_stride, head_stride, slot_stride;
   int seqs, heads, group, tiles, dim, cols, pages, page_size, max_len, max_keys, window, wgs;
-  bool split;
   float scale, softcap;
   FastDiv page_div, units_div, tiles_div, wgs_div, quads_div;  // units: of one sequence
 };
@@ -183,8 +182,8 @@ struct Place {
 // No unit is cut within this many grains of its ends, for shares of `per` grains: a cut costs two partials
 // and their join, about as much as four grains, so larger shares leave small units whole (8 x 8 units of 6 to
 // 368 grains, per = 4: 22.5 us with 2, 25.4 with 1; 12 x 5 units of 11 grains, per = 2: 14.5 us with 1, 15.8
-// with 2). Units of fewer than kCut are not cut (8 units of four grains: 10.6 us, in four workgroups each 11.9;
-// of five: 14.0 whole, 12.0 cut).
+// with 2). Units of fewer than kCut are not cut (8 units of four grains: 9.4 us, in four workgroups each 11.9;
+// of five: 13.3 whole, 11.1 cut).
 constexpr int kCut = 5;
 MX_DEV int least_of(uint32_t per, int grains) { return grains < kCut ? grains : (int)min(max(per / 2u, 1u), 4u); }
 
@@ -244,51 +243,60 @@ MX_DEV float soft_cap(float s, float c) {
   return c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// Tiles of a wave on their way: two, or one of D = 256, whose registers would not hold a second.
-constexpr int tiles_ahead(int D) { return D == 256 ? 1 : 2; }
-// Of D = 256, 16-bit rows take more than 256 registers (16 x 8192 x 4 fp16: 88 us, spilled into 256 of them 101;
-// E4M3 fits: 64 us against 69). D = 64 fits three waves (78 x 16 short rows E4M3: 17 us, 20 with two, 24 spilled
-// into four).
-constexpr int waves_per_simd(int D, bool mx8) { return D == 256 && !mx8 ? 1 : D == 64 ? 3 : 2; }
+// Tiles of a wave on their way: two, or one of D = 256, whose registers would not hold a second; and one where
+// workgroups take whole units, a few tiles of a wave, whose time is the code's length (8 x 500 keys: 9.4 us, 10.0
+// with two).
+constexpr int tiles_ahead(int D, bool split) { return D == 256 || !split ? 1 : 2; }
+// A query's 32 registers would be spilled of D = 256: a lane keeps them in LDS, where the merge's rows come later.
+constexpr bool query_in_lds(int D) { return D == 256; }
+// Shares of D = 256 16-bit rows take more than 256 registers (16 x 8192 x 4 fp16: 88 us, spilled into 256 of them
+// 101; E4M3 fits: 64 us against 69), which whole units, small and many, do better without (200 x 4 rows of 30 keys:
+// 15 us against 25). Shares of D = 64 fit three waves (78 x 16 short rows E4M3: 17 us, 20 with two, 24 spilled into four).
+constexpr int waves_per_simd(int D, bool mx8, bool split) { return !split ? 2 : D == 64 ? 3 : D == 256 && !mx8 ? 1 : 2; }
 
 // D: 64, 128 or 256, the head size rounded up. T: type of q, out and the arithmetic. MX8: E4M3 cache.
 // PAGED16: page_size % 16 == 0, so that the 16 keys of half a tile lie in one page: their place is a
 // buffer descriptor in scalar registers, whose size also turns keys past the end, missing pages and
 // elements past dim into zeros. For other page sizes a lane works out one key's place and the others
 // read it from LDS.
-template <int D, typename T, bool MX8, bool PAGED16>
-__global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kernel(Args) {
+// SPLIT: workgroups take shares of the grains and join what they cut; else one takes a whole unit, and the code
+// of shares and joins, whose instructions would be waited for, is left out (4 x 12 rows of 30 keys: 5.6 us, 6.4
+// with it; eight waves for a unit were slower than four: 8 x 500 keys 11.1 us against 10.0).
+template <int D, typename T, bool MX8, bool PAGED16, bool SPLIT>
+__global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decode_kernel(Args) {
   typedef typename Vec<T>::x8 x8;
   constexpr float kShift = Vec<T>::kShift;
-  constexpr int kSteps = D / 32;          // matrix instructions of one score tile
-  constexpr int kLoads = MX8 ? D / 64 : kSteps;  // 16-byte loads of a key's row
+  constexpr int kGrains = D / 32;          // matrix instructions of one score tile
+  constexpr int kLoads = MX8 ? D / 64 : kGrains;  // 16-byte loads of a key's row
   constexpr int kRuns = D == 256 ? 2 : 1; // runs of kRow elements of V per lane and key
   constexpr int kRow = D == 64 ? 4 : 8;
   constexpr int kOut = D / 16;            // accumulators
   constexpr int kSize = MX8 ? 1 : 2;      // bytes of an element
-  constexpr int kAhead = tiles_ahead(D);
+  constexpr int kAhead = tiles_ahead(D, SPLIT);
   constexpr int kBlock = 32;              // tiles of a wave whose pages it looks up at a time
-  extern __shared__ float lds[];          // merge: [kWaves / 2][head][D + kPad]; join: sums, then [head][kFan] weights
+  extern __shared__ float lds[];          // queries: [wave][step][lane]; merge: [kWaves / 2][head][D + kPad]; join: sums, then [head][kFan] weights
   __shared__ float wave_m[kWaves][16], wave_l[kWaves][16], head_m[16], head_l[16];
   __shared__ int is_last;
-  constexpr bool kQueryInLds = D == 256;  // its 32 registers would be spilled: a wave's lanes keep them here
-  __shared__ u32x4 query_of[kQueryInLds ? kWaves : 1][kQueryInLds ? kSteps : 1][64];
+  constexpr bool kQueryInLds = query_in_lds(D);
+  u32x4* const query = reinterpret_cast<u32x4*>(lds) + (threadIdx.x >> 6) * kGrains * 64 + (threadIdx.x & 63);
   __shared__ int64_t place_of[PAGED16 ? 1 : kWaves][2][kTile];  // of the keys of a wave's two tiles
 
   Kernarg* const args = (Kernarg*)__builtin_amdgcn_kernarg_segment_ptr();
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   const int units = args->heads * args->tiles;
-  Place at, end;
+  Place at, end = {};
   uint32_t per = 1u;
-  if (args->split) {
+  if constexpr (SPLIT) {
     per = share_of(*args, units, at, end);
   } else {
     const int b = (int)copy_of(args->units_div).div(blockIdx.x);
     at = Place{b, (int)blockIdx.x - b * units, 0, 0};
-    end = at.unit + 1 < units ? Place{at.b, at.unit + 1, 0, 0} : Place{at.b + 1, 0, 0, 0};
   }
 
-  while (at.b < end.b || (at.b == end.b && (at.unit < end.unit || (at.unit == end.unit && at.grain < end.grain)))) {
+  for (;;) {
+    if constexpr (SPLIT) {
+      if (!(at.b < end.b || (at.b == end.b && (at.unit < end.unit || (at.unit == end.unit && at.grain < end.grain))))) break;
+    }
     Kernarg& a = *fresh(args);
     const int b = at.b, dim = a.dim;
     const int hk = (int)copy_of(a.tiles_div).div((uint32_t)at.unit), ht = at.unit - hk * a.tiles;
@@ -310,26 +318,26 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
     if (from_zero) page_ahead = page_at(ahead + (PAGED16 ? (lane >> 1) * kGrain + (lane & 1) * 16 : lane & (kTile - 1)));
 
     // Query fragments: column c, the elements that this lane's K loads hold; zeros past the heads and past dim.
-    x8 qf[kQueryInLds ? 1 : kSteps];
+    x8 qf[kQueryInLds ? 1 : kGrains];
     {
       const T* q = (const T*)a.q + (int64_t)b * a.qt + (int64_t)(first_head + (c < n_heads ? c : 0)) * a.qh;
-      u32x4 w[kSteps];
+      u32x4 w[kGrains];
 #pragma unroll
-      for (int s = 0; s < kSteps; s++) {
+      for (int s = 0; s < kGrains; s++) {
         const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
         w[s] = *reinterpret_cast<const u32x4*>(q + (d < dim ? d : 0));
       }
 #pragma unroll
-      for (int s = 0; s < kSteps; s++) {
+      for (int s = 0; s < kGrains; s++) {
         const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
         if (c >= n_heads || d >= dim) w[s] = (u32x4){0u, 0u, 0u, 0u};
-        if constexpr (kQueryInLds) query_of[wave][s][lane] = w[s];
+        if constexpr (kQueryInLds) query[64 * s] = w[s];
         else qf[s] = __builtin_bit_cast(x8, w[s]);
       }
     }
     Row row = row_of(a, length, a.starts ? start : 0);
     row = Row{uniform(row.lo), uniform(row.hi), from_zero ? 0 : uniform(row.base), uniform(row.grains)};
-    const int stop = b == end.b && at.unit == end.unit ? end.grain : row.grains;
+    const int stop = SPLIT && b == end.b && at.unit == end.unit ? end.grain : row.grains;
     const int from = row.base + at.grain * kGrain, to = min(row.hi, row.base + stop * kGrain), lo = row.lo;
 
     // Byte offsets of this lane's loads within 16 keys' rows.
@@ -496,9 +504,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
         // S^T: keys 4 g + i of half h, head c.
         f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-        for (int st = 0; st < kSteps; st++) {
+        for (int st = 0; st < kGrains; st++) {
           x8 q;
-          if constexpr (kQueryInLds) q = __builtin_bit_cast(x8, query_of[wave][st][lane]);
+          if constexpr (kQueryInLds) q = __builtin_bit_cast(x8, query[64 * st]);
           else q = qf[st];
 #pragma unroll
           for (int h = 0; h < 2; h++) {
@@ -639,7 +647,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
     const auto put_lse = [&](int h, float top, float sum) {
       if (z.lse) z.lse[(int64_t)b * z.heads * z.group + first_head + h] = sum == 0.f ? -INFINITY : kLn2 * (top - kShift + __log2f(sum));
     };
-    const bool whole = at.grain == 0 && stop == row.grains;
+    const bool whole = !SPLIT || (at.grain == 0 && stop == row.grains);
     // Partials, one for a share that begins within a unit and one for a unit that ends past the share:
     // [16][dim] outputs, then [16] {maximum, sum}.
     const uint32_t rows_at = (uint32_t)(16 * dim * 4), slot_size = rows_at + 16 * 8;
@@ -667,6 +675,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
     // barrier and the counter's increment, so the last one (which takes the counter back to 0) sees all.
     // A partial's counter is its group's first one's. The code is kept short: its instructions come from
     // memory, as each workgroup runs it once.
+    if constexpr (!SPLIT) break;
     if (!whole) {
       const uint32_t u0 = at.at + (uint32_t)(at.unit * row.grains), least = least_of(per, row.grains);
       const int first = uniform((int)((u0 + least + per - 1) / per)) - 1;  // the unit's first workgroup
@@ -781,10 +790,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8)) void decode_kerne
 
 // ---- host -----------------------------------------------------------------------------------
 
-// LDS bytes: the merge's rows, or the join's weights and sums.
+// LDS bytes: the merge's rows, the queries, or the join's weights and sums.
 size_t lds_bytes(int D, int n_heads, bool split) {
   const size_t merge = (size_t)(kWaves / 2) * n_heads * (D + kPad) * 4, weights = (size_t)(n_heads * kFan + 4 * kThreads) * 4;
-  return split && weights > merge ? weights : merge;
+  const size_t query = query_in_lds(D) ? (size_t)kWaves * D * 32 : 0;
+  return std::max(std::max(merge, query), split ? weights : 0);
 }
 
 struct Plan {
@@ -811,7 +821,7 @@ Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
   const int64_t grains = ceil_div(span, (int64_t)kGrain), wgs = p.units * grains;
   if (grains < kCut || p.units * grains >= (int64_t)1 << 30) return p;  // (the device counts in 32 bits)
   const int D = c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256;
-  const int most = kCUs * (tiles_ahead(D) * kGrain * 2 * D * (c->fmt == MX_E4M3 ? 1 : 2) < 131072 ? 2 : 1);
+  const int most = kCUs * (tiles_ahead(D, true) * kGrain * 2 * D * (c->fmt == MX_E4M3 ? 1 : 2) < 131072 ? 2 : 1);
   p.wgs = (int)(wgs < most ? wgs : most);
   p.bytes = kCounterBytes + (size_t)(2 * p.wgs) * 16 * (c->dim + 2) * 4;
   return p;
@@ -822,18 +832,24 @@ bool sizes_ok(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
          max_len < 1 << 30 && window >= 0 && (int64_t)seqs * q_heads < (int64_t)1 << 24;
 }
 
+template <int D, typename T, bool MX8, bool SPLIT>
+void launch(const Args& a, unsigned wgs, hipStream_t st) {
+  const size_t lds = lds_bytes(D, a.group < 16 ? a.group : 16, SPLIT);
+  if (a.page_size % 16 == 0) hipLaunchKernelGGL((decode_kernel<D, T, MX8, true, SPLIT>), dim3(wgs), dim3(kThreads), lds, st, a);
+  else hipLaunchKernelGGL((decode_kernel<D, T, MX8, false, SPLIT>), dim3(wgs), dim3(kThreads), lds, st, a);
+}
+
 template <int D, typename T, bool MX8>
-void launch(const Args& a, dim3 grid, hipStream_t st) {
-  const size_t lds = lds_bytes(D, a.group < 16 ? a.group : 16, a.split);
-  if (a.page_size % 16 == 0) hipLaunchKernelGGL((decode_kernel<D, T, MX8, true>), grid, dim3(kThreads), lds, st, a);
-  else hipLaunchKernelGGL((decode_kernel<D, T, MX8, false>), grid, dim3(kThreads), lds, st, a);
+void launch_split(const Args& a, const Plan& p, bool split, hipStream_t st) {
+  if (split) launch<D, T, MX8, true>(a, (unsigned)p.wgs, st);
+  else launch<D, T, MX8, false>(a, (unsigned)p.units, st);
 }
 
 template <typename T, bool MX8>
-void launch_dim(const Args& a, dim3 grid, hipStream_t st) {
-  if (a.dim <= 64) launch<64, T, MX8>(a, grid, st);
-  else if (a.dim <= 128) launch<128, T, MX8>(a, grid, st);
-  else launch<256, T, MX8>(a, grid, st);
+void launch_dim(const Args& a, const Plan& p, bool split, hipStream_t st) {
+  if (a.dim <= 64) launch_split<64, T, MX8>(a, p, split, st);
+  else if (a.dim <= 128) launch_split<128, T, MX8>(a, p, split, st);
+  else launch_split<256, T, MX8>(a, p, split, st);
 }
 
 }  // namespace
@@ -867,9 +883,9 @@ extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads*
   a.out = out->data, a.ot = out->token_stride, a.oh = out->head_stride;
   a.lse = lse;
   a.table = table->pages, a.cols = table->cols, a.lengths = lengths, a.starts = starts;
-  a.split = p.wgs > 0 && workspace && workspace_bytes >= p.bytes;  // else a workgroup takes a whole unit
+  const bool split = p.wgs > 0 && workspace && workspace_bytes >= p.bytes;  // else a workgroup takes a whole unit
   a.wgs = p.wgs;
-  if (a.split) {
+  if (split) {
     a.counters = (uint32_t*)workspace;
     a.partial = (float*)((uint8_t*)workspace + kCounterBytes);
   }
@@ -881,14 +897,13 @@ extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads*
   a.page_div = FastDiv((uint32_t)cache->page_size);
   a.units_div = FastDiv((uint32_t)(cache->heads * p.tiles));
   a.tiles_div = FastDiv((uint32_t)p.tiles);
-  a.wgs_div = FastDiv((uint32_t)(a.split ? p.wgs : 1));
+  a.wgs_div = FastDiv((uint32_t)(split ? p.wgs : 1));
   a.quads_div = FastDiv((uint32_t)cache->dim / 4);
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
-  const dim3 grid((unsigned)(a.split ? p.wgs : p.units));
-  if (f == MX_F16 && mx8) launch_dim<_Float16, true>(a, grid, st);
-  else if (f == MX_F16) launch_dim<_Float16, false>(a, grid, st);
-  else if (mx8) launch_dim<__bf16, true>(a, grid, st);
-  else launch_dim<__bf16, false>(a, grid, st);
+  if (f == MX_F16 && mx8) launch_dim<_Float16, true>(a, p, split, st);
+  else if (f == MX_F16) launch_dim<_Float16, false>(a, p, split, st);
+  else if (mx8) launch_dim<__bf16, true>(a, p, split, st);
+  else launch_dim<__bf16, false>(a, p, split, st);
   return sync_check(launch_status(), st);
 }
