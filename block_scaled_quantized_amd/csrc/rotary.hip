@@ -8,6 +8,13 @@
 // pos * f / 2 pi loses about 2^-52 of its value (2^20 positions: 2^-32 turns), where 32 bits would
 // lose the phase of far positions altogether; after the reduction to half a turn an fp32 sine and
 // cosine are exact to 2 ulp.
+//
+// Rows move in 16-byte units whatever rot_dim is. Halves of whole units are loaded as pairs of units,
+// neighbouring pairs lie in one; halves that begin within a unit (rot_dim / 2 not a multiple of it) are
+// staged in LDS, where each element finds its partner. Measured, 4096 tokens x 32 heads x 128 bf16, 67 MB:
+// 11.9 us with rot_dim = 128 in halves, 12.5 us in pairs, 17 us with rot_dim = 126 in halves (34 us one
+// pair at a time). Append of 8191 tokens, 32 query and 8 cache heads of 128 bf16, 201 MB: 37 us, 5.4 TB/s; into an
+// E4M3 cache 4096 tokens take 22 us.
 #include <cmath>
 #include <type_traits>
 
@@ -19,8 +26,10 @@ using namespace mx;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTrig = 512;  // (token, pair) angles of a workgroup
-constexpr int kStage = 8192;   // 16-bit elements of rotated keys that a workgroup stages
+constexpr int kMaxTrig = 512;        // (token, pair) angles of a workgroup
+constexpr int kStageBytes = 16384;   // rows that a workgroup stages in LDS
+// How a head's pairs lie: halves of whole 16-byte units; neighbours; halves that begin within a unit.
+enum Layout { kHalves, kNeighbours, kOddHalves };
 
 template <typename T>
 struct Unit {  // 16 bytes of elements
@@ -81,27 +90,32 @@ MX_DEV void fill_trig(const Rotation& r, const int32_t* __restrict__ pos, int t0
   }
 }
 
-// How a head's dim elements are dealt to threads: `pairs` items that rotate, then `tail` items of
-// elements that are copied. VEC: an item moves whole 16-byte units (HALF: one of each half's, PAIRS:
-// one); else one pair or one element.
+// How a head's 16-byte units are dealt to threads: `pairs` items that rotate (kHalves: a unit of each half
+// together), then those that are copied.
 struct Split {
   int pairs, items;
 };
 
-// A workgroup's rows: tokens t0 .. t0 + tokens - 1 times heads h0 .. h0 + heads - 1. store(token, head,
-// element, values, count) takes a unit or single elements. COPY_TAIL: whether copied elements need a store.
-template <typename T, bool PAIRS, bool VEC, bool STREAM, typename Store>
-MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, int t0, int tokens, const T* __restrict__ x,
-                        int64_t xt, int64_t xh, int h0, int heads, Split sp, bool copy_tail, float2* trig, Store store) {
+// A workgroup's rows: tokens t0 .. t0 + tokens - 1 times heads h0 .. h0 + heads - 1 of x.
+template <typename T>
+struct Rows {
+  const T* x;
+  int64_t xt, xh;
+  int t0, tokens, h0, heads;
+  MX_DEV const T* at(int t, int h) const { return x + (int64_t)(t0 + t) * xt + (int64_t)(h0 + h) * xh; }
+};
+
+// Units to store(token, head, element, unit). copy_tail: whether copied units need a store. Not for kOddHalves.
+template <typename T, Layout L, bool STREAM, typename Store>
+MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, const Rows<T>& z, Split sp, bool copy_tail,
+                        float2* trig, Store store) {
   constexpr int kBatch = batch_of(STREAM);
   constexpr int U = Unit<T>::N;
   const int per = kThreads / sp.items;  // rows of one pass
   const int item = threadIdx.x % sp.items, r0 = threadIdx.x / sp.items;
   const bool turns = item < sp.pairs, mine = r0 < per && (turns || copy_tail);
-  const int rows = tokens * heads, half = rot.half;
-  // first element, and the second half's for HALF
-  const int a = VEC ? (turns ? U * item : 2 * half + U * (item - sp.pairs))
-                    : (turns ? (PAIRS ? 2 * item : item) : 2 * half + item - sp.pairs);
+  const int rows = z.tokens * z.heads, half = rot.half;
+  const int a = L == kNeighbours || turns ? U * item : 2 * half + U * (item - sp.pairs);  // first element
   bool ready = false;
   for (int base = r0; base - r0 < rows; base += per * kBatch) {  // the same number of turns for every thread
     Unit<T> lo[kBatch], hi[kBatch];
@@ -109,21 +123,16 @@ MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, in
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
       const int row = base + u * per;
-      tok[u] = row / heads;
-      head[u] = row - tok[u] * heads;
+      tok[u] = row / z.heads;
+      head[u] = row - tok[u] * z.heads;
       if (mine && row < rows) {
-        const T* p = x + (int64_t)(t0 + tok[u]) * xt + (int64_t)(h0 + head[u]) * xh + a;
-        if constexpr (VEC) {
-          lo[u] = load_unit<STREAM>(p);
-          if (!PAIRS && turns) hi[u] = load_unit<STREAM>(p + half);
-        } else {
-          lo[u].e[0] = p[0];
-          if (turns) hi[u].e[0] = p[PAIRS ? 1 : half];
-        }
+        const T* p = z.at(tok[u], head[u]) + a;
+        lo[u] = load_unit<STREAM>(p);
+        if (L == kHalves && turns) hi[u] = load_unit<STREAM>(p + half);
       }
     }
     if (!ready) {
-      fill_trig(rot, pos, t0, tokens, trig);
+      fill_trig(rot, pos, z.t0, z.tokens, trig);
       __syncthreads();
       ready = true;
     }
@@ -131,18 +140,19 @@ MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, in
     for (int u = 0; u < kBatch; u++) {
       if (!mine || base + u * per >= rows) continue;
       if (turns) {
-        const float2* cs = trig + tok[u] * half + (VEC ? (PAIRS ? item * (U / 2) : item * U) : item);
-        if constexpr (VEC && PAIRS) {
+        const float2* cs = trig + tok[u] * half + (L == kNeighbours ? item * (U / 2) : item * U);
+        if constexpr (L == kNeighbours) {
 #pragma unroll
           for (int i = 0; i < U / 2; i++) {
             const float p = to_f32(lo[u].e[2 * i]), q = to_f32(lo[u].e[2 * i + 1]);
-            const float2 w = cs[i];
-            lo[u].e[2 * i] = turn_a<T>(p, q, w);
-            lo[u].e[2 * i + 1] = turn_b<T>(p, q, w);
+            const float2 w = cs[i];  // (past the last pair: of the next token, or the padding, and unused)
+            const bool turned = item * (U / 2) + i < half;
+            lo[u].e[2 * i] = turned ? turn_a<T>(p, q, w) : lo[u].e[2 * i];
+            lo[u].e[2 * i + 1] = turned ? turn_b<T>(p, q, w) : lo[u].e[2 * i + 1];
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < (VEC ? U : 1); i++) {
+          for (int i = 0; i < U; i++) {
             const float p = to_f32(lo[u].e[i]), q = to_f32(hi[u].e[i]);
             const float2 w = cs[i];
             lo[u].e[i] = turn_a<T>(p, q, w);
@@ -151,15 +161,48 @@ MX_DEV void rotate_rows(const Rotation& rot, const int32_t* __restrict__ pos, in
         }
       }
       store(tok[u], head[u], a, lo[u]);
-      if (turns && !(VEC && PAIRS)) store(tok[u], head[u], a + (PAIRS ? 1 : half), hi[u]);
+      if (L == kHalves && turns) store(tok[u], head[u], a + half, hi[u]);
     }
   }
 }
 
-template <typename T, bool VEC>
-MX_DEV void put(T* p, const Unit<T>& v) {
-  if constexpr (VEC) *reinterpret_cast<Unit<T>*>(p) = v;
-  else p[0] = v.e[0];
+// The rows as they are to LDS [row][dim] in units, and the angles; the caller synchronises.
+template <typename T, bool STREAM>
+MX_DEV void stage_rows(const Rotation& rot, const int32_t* __restrict__ pos, const Rows<T>& z, int dim, float2* trig, T* stage) {
+  constexpr int kBatch = batch_of(STREAM), U = Unit<T>::N;
+  const int units = dim / U, per = kThreads / units, unit = threadIdx.x % units, r0 = threadIdx.x / units;
+  const int rows = z.tokens * z.heads;
+  for (int base = r0; base < rows && r0 < per; base += per * kBatch) {
+    Unit<T> v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      const int row = base + u * per, t = row / z.heads;
+      if (row < rows) v[u] = load_unit<STREAM>(z.at(t, row - t * z.heads) + U * unit);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; u++)
+      if (base + u * per < rows) *reinterpret_cast<Unit<T>*>(stage + (base + u * per) * dim + U * unit) = v[u];
+  }
+  fill_trig(rot, pos, z.t0, z.tokens, trig);
+}
+
+// The unit from element e0 of a staged row, turned (kOddHalves): each element's partner is read by itself, as its unit
+// begins elsewhere.
+template <typename T>
+MX_DEV Unit<T> turned_unit(const T* row, int e0, int half, const float2* cs) {
+  Unit<T> v = *reinterpret_cast<const Unit<T>*>(row + e0);
+  if (e0 >= 2 * half) return v;
+#pragma unroll
+  for (int i = 0; i < Unit<T>::N; i++) {
+    const int e = e0 + i;
+    const bool second = e >= half;
+    const int at = second ? e - half : e + half;  // within the row, whatever e
+    const float2 w = cs[min(second ? e - half : e, half - 1)];
+    // turn_b's step, or turn_a's: -(b sin) is b (-sin)
+    const T turned = round_to<T>(__builtin_fmaf(to_f32(v.e[i]), w.x, to_f32(row[at]) * (second ? w.y : -w.y)));
+    v.e[i] = e < 2 * half ? turned : v.e[i];
+  }
+  return v;
 }
 
 struct RopeArgs {
@@ -173,23 +216,32 @@ struct RopeArgs {
   bool stream;
 };
 
-template <typename T, bool PAIRS, bool VEC, bool STREAM>
-MX_DEV void rope_block(const RopeArgs& a, int block, float2* trig) {
+template <typename T, Layout L, bool STREAM>
+MX_DEV void rope_block(const RopeArgs& a, int block, float2* trig, T* stage) {
+  constexpr int U = Unit<T>::N;
   const int g = block % a.groups, t0 = (block / a.groups) * a.tile_t, h0 = g * a.tile_h;
-  T* out = (T*)a.out;
-  rotate_rows<T, PAIRS, VEC, STREAM>(a.rot, a.pos, t0, min(a.tile_t, a.tokens - t0), (const T*)a.x, a.xt, a.xh, h0,
-                             min(a.tile_h, a.heads - h0), a.split, a.x != a.out, trig,
-                             [&](int t, int h, int e, const Unit<T>& v) {
-                               T* p = out + (int64_t)(t0 + t) * a.ot + (int64_t)(h0 + h) * a.oh + e;
-                               if constexpr (VEC) store_unit(p, v);
-                               else p[0] = v.e[0];
-                             });
+  const Rows<T> z = {(const T*)a.x, a.xt, a.xh, t0, min(a.tile_t, a.tokens - t0), h0, min(a.tile_h, a.heads - h0)};
+  const auto out = [&](int t, int h) -> T* { return (T*)a.out + (int64_t)(t0 + t) * a.ot + (int64_t)(h0 + h) * a.oh; };
+  if constexpr (L != kOddHalves) {
+    rotate_rows<T, L, STREAM>(a.rot, a.pos, z, a.split, a.x != a.out, trig,
+                              [&](int t, int h, int e, const Unit<T>& v) { store_unit(out(t, h) + e, v); });
+  } else {
+    const int units = a.split.items, dim = U * units, per = kThreads / units, unit = threadIdx.x % units, r0 = threadIdx.x / units;
+    stage_rows<T, STREAM>(a.rot, a.pos, z, dim, trig, stage);
+    __syncthreads();
+    if (r0 >= per || (unit >= a.split.pairs && a.x == a.out)) return;
+    for (int row = r0; row < z.tokens * z.heads; row += per) {
+      const int t = row / z.heads;
+      store_unit(out(t, row - t * z.heads) + U * unit, turned_unit(stage + row * dim, U * unit, a.rot.half, trig + t * a.rot.half));
+    }
+  }
 }
 
-template <typename T, bool PAIRS, bool VEC, bool STREAM>
+template <typename T, Layout L, bool STREAM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
-  __shared__ float2 trig[kMaxTrig];
-  rope_block<T, PAIRS, VEC, STREAM>(a, blockIdx.x, trig);
+  __shared__ float2 trig[kMaxTrig + 8];
+  __shared__ __attribute__((aligned(16))) T stage[L == kOddHalves ? kStageBytes / sizeof(T) : 1];
+  rope_block<T, L, STREAM>(a, blockIdx.x, trig, stage);
 }
 
 // ---- append ---------------------------------------------------------------------------------
@@ -262,14 +314,14 @@ MX_DEV void write_unit(const Unit<T>& v, bool mx8, uint8_t* codes, uint8_t* scal
   if (at % 32 == 0) scales[at / 32] = (uint8_t)E;
 }
 
-template <typename T, bool PAIRS, bool VEC, bool STREAM>
+template <typename T, Layout L, bool STREAM>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8) {
-  __shared__ float2 trig[kMaxTrig];
-  __shared__ T stage[kStage];
+  __shared__ float2 trig[kMaxTrig + 8];
+  __shared__ __attribute__((aligned(16))) T stage[kStageBytes / sizeof(T)];
   __shared__ int64_t slot[kMaxTrig];
   int block = blockIdx.x;
   if (block < a.q_blocks) {
-    rope_block<T, PAIRS, VEC, STREAM>(a.q, block, trig);
+    rope_block<T, L, STREAM>(a.q, block, trig, stage);
     return;
   }
   block -= a.q_blocks;
@@ -278,11 +330,15 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8
   const int g = block % a.k.groups, t0 = (block / a.k.groups) * a.k.tile_t, h0 = g * a.k.tile_h;
   const int tokens = min(a.k.tile_t, a.k.tokens - t0), heads = min(a.k.tile_h, a.k.heads - h0);
   fill_slots(a, t0, tokens, slot);
-  if (key && a.turn)
-    rotate_rows<T, PAIRS, VEC, STREAM>(a.k.rot, a.k.pos, t0, tokens, (const T*)a.k.x, a.k.xt, a.k.xh, h0, heads, a.k.split, true, trig,
-                               [&](int t, int h, int e, const Unit<T>& v) {
-                                 put<T, VEC>(stage + (t * heads + h) * a.dim + e, v);
-                               });
+  if (key && a.turn) {
+    const Rows<T> z = {(const T*)a.k.x, a.k.xt, a.k.xh, t0, tokens, h0, heads};
+    if constexpr (L == kOddHalves)
+      stage_rows<T, STREAM>(a.k.rot, a.k.pos, z, a.dim, trig, stage);
+    else
+      rotate_rows<T, L, STREAM>(a.k.rot, a.k.pos, z, a.k.split, true, trig, [&](int t, int h, int e, const Unit<T>& v) {
+        *reinterpret_cast<Unit<T>*>(stage + (t * heads + h) * a.dim + e) = v;
+      });
+  }
   __syncthreads();
   // Rows go out in units of 8 elements; dim / 8 divides nothing in general, so threads past the last
   // whole row of a pass idle (they still take part in the lane exchange).
@@ -295,7 +351,9 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8
     const bool mine = r0 < per && row < tokens * heads;
     const int t = mine ? row / heads : 0, h = mine ? row - t * heads : 0;
     Unit<T> v = {};
-    if (mine)
+    if (mine && L == kOddHalves && key && a.turn)
+      v = turned_unit(stage + row * a.dim, 8 * unit, a.k.rot.half, trig + t * a.k.rot.half);
+    else if (mine)
       v = key && a.turn ? *reinterpret_cast<const Unit<T>*>(stage + row * a.dim + 8 * unit)
                         : load_unit<false>(x + (int64_t)(t0 + t) * xt + (int64_t)(h0 + h) * xh + 8 * unit);
     const int64_t s = mine ? slot[t] : -1;
@@ -305,18 +363,13 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8
 
 // ---- host -----------------------------------------------------------------------------------
 
-bool vec_ok(int layout, int rot_dim, int unit) { return (layout == MXROPE_HALF ? rot_dim / 2 : rot_dim) % unit == 0; }
+Layout layout_of(int layout, int rot_dim, int unit) {
+  return layout == MXROPE_PAIRS ? kNeighbours : rot_dim / 2 % unit == 0 ? kHalves : kOddHalves;
+}
 
-Split split_of(int layout, int rot_dim, int dim, int unit, bool vec) {
-  Split s;
-  if (vec) {
-    s.pairs = layout == MXROPE_HALF ? rot_dim / 2 / unit : rot_dim / unit;
-    s.items = s.pairs + (dim - rot_dim) / unit;
-  } else {
-    s.pairs = rot_dim / 2;
-    s.items = s.pairs + dim - rot_dim;
-  }
-  return s;
+Split split_of(Layout layout, int rot_dim, int dim, int unit) {
+  if (layout == kHalves) return {rot_dim / 2 / unit, rot_dim / 2 / unit + (dim - rot_dim) / unit};
+  return {ceil_div(rot_dim, unit), dim / unit};
 }
 
 // Tokens and heads of a workgroup. max_rows bounds tile_t * tile_h.
@@ -343,39 +396,39 @@ int check_rope(const mxrope* r, int dim) {
 }
 
 RopeArgs rope_args(const mxrope* r, int tokens, int dim, const mx_heads* x, const mx_heads* out, const int32_t* pos, int inverse,
-                   int unit, bool vec) {
+                   int unit, Layout layout) {
   RopeArgs a = {};
   a.rot = {r ? r->freq : nullptr, r ? r->rot_dim / 2 : 0, r ? r->factor : 1.0f, inverse ? -1.0f : 1.0f};
   a.pos = pos;
   a.x = x->data, a.xt = x->token_stride, a.xh = x->head_stride;
   if (out) a.out = out->data, a.ot = out->token_stride, a.oh = out->head_stride;
   a.tokens = tokens, a.heads = x->heads;
-  a.split = split_of(r ? r->layout : MXROPE_HALF, r ? r->rot_dim : 0, dim, unit, vec);
+  a.split = split_of(layout, r ? r->rot_dim : 0, dim, unit);
   return a;
 }
 
+template <typename T, Layout L>
+void rope_launch(const RopeArgs& a, dim3 grid, hipStream_t st) {
+  if (a.stream) hipLaunchKernelGGL((rope_kernel<T, L, true>), grid, dim3(kThreads), 0, st, a);
+  else hipLaunchKernelGGL((rope_kernel<T, L, false>), grid, dim3(kThreads), 0, st, a);
+}
 template <typename T>
-void rope_launch(const RopeArgs& a, bool pairs, bool vec, dim3 grid, hipStream_t st) {
-  const bool stream = vec && a.stream;
-  const dim3 block(kThreads);
-  if (pairs && stream) hipLaunchKernelGGL((rope_kernel<T, true, true, true>), grid, block, 0, st, a);
-  else if (pairs && vec) hipLaunchKernelGGL((rope_kernel<T, true, true, false>), grid, block, 0, st, a);
-  else if (pairs) hipLaunchKernelGGL((rope_kernel<T, true, false, false>), grid, block, 0, st, a);
-  else if (stream) hipLaunchKernelGGL((rope_kernel<T, false, true, true>), grid, block, 0, st, a);
-  else if (vec) hipLaunchKernelGGL((rope_kernel<T, false, true, false>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((rope_kernel<T, false, false, false>), grid, block, 0, st, a);
+void rope_launch(const RopeArgs& a, Layout layout, dim3 grid, hipStream_t st) {
+  if (layout == kHalves) rope_launch<T, kHalves>(a, grid, st);
+  else if (layout == kNeighbours) rope_launch<T, kNeighbours>(a, grid, st);
+  else rope_launch<T, kOddHalves>(a, grid, st);
 }
 
+template <typename T, Layout L>
+void append_launch(const AppendArgs& a, bool mx8, dim3 grid, hipStream_t st) {
+  if (a.k.stream) hipLaunchKernelGGL((append_kernel<T, L, true>), grid, dim3(kThreads), 0, st, a, mx8);
+  else hipLaunchKernelGGL((append_kernel<T, L, false>), grid, dim3(kThreads), 0, st, a, mx8);
+}
 template <typename T>
-void append_launch(const AppendArgs& a, bool pairs, bool vec, bool mx8, dim3 grid, hipStream_t st) {
-  const bool stream = vec && a.k.stream;
-  const dim3 block(kThreads);
-  if (pairs && stream) hipLaunchKernelGGL((append_kernel<T, true, true, true>), grid, block, 0, st, a, mx8);
-  else if (pairs && vec) hipLaunchKernelGGL((append_kernel<T, true, true, false>), grid, block, 0, st, a, mx8);
-  else if (pairs) hipLaunchKernelGGL((append_kernel<T, true, false, false>), grid, block, 0, st, a, mx8);
-  else if (stream) hipLaunchKernelGGL((append_kernel<T, false, true, true>), grid, block, 0, st, a, mx8);
-  else if (vec) hipLaunchKernelGGL((append_kernel<T, false, true, false>), grid, block, 0, st, a, mx8);
-  else hipLaunchKernelGGL((append_kernel<T, false, false, false>), grid, block, 0, st, a, mx8);
+void append_launch(const AppendArgs& a, Layout layout, bool mx8, dim3 grid, hipStream_t st) {
+  if (layout == kHalves) append_launch<T, kHalves>(a, mx8, grid, st);
+  else if (layout == kNeighbours) append_launch<T, kNeighbours>(a, mx8, grid, st);
+  else append_launch<T, kOddHalves>(a, mx8, grid, st);
 }
 
 }  // namespace
@@ -426,16 +479,16 @@ extern "C" int mxrope_run(int f, const mxrope* rope, int tokens, int dim, const 
   if (int s = check_heads(out, bytes)) return s;
   if (x->heads != out->heads) return MX_ERR_SHAPE;
   if (x->data == out->data && (x->token_stride != out->token_stride || x->head_stride != out->head_stride)) return MX_ERR_SHAPE;
-  const bool pairs = rope->layout == MXROPE_PAIRS, vec = vec_ok(rope->layout, rope->rot_dim, 16 / bytes);
-  RopeArgs a = rope_args(rope, tokens, dim, x, out, positions, inverse, 16 / bytes, vec);
+  const Layout layout = layout_of(rope->layout, rope->rot_dim, 16 / bytes);
+  RopeArgs a = rope_args(rope, tokens, dim, x, out, positions, inverse, 16 / bytes, layout);
   a.stream = 2ll * tokens * x->heads * dim * bytes >= kStreamBytes;
-  tile(a, 1 << 20);
+  tile(a, layout == kOddHalves ? kStageBytes / (dim * bytes) : 1 << 20);
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
   const dim3 grid((unsigned)blocks_of(a));  // at most tokens + 1024
-  if (f == MX_F16) rope_launch<_Float16>(a, pairs, vec, grid, st);
-  else if (f == MX_BF16) rope_launch<__bf16>(a, pairs, vec, grid, st);
-  else rope_launch<float>(a, pairs, vec, grid, st);
+  if (f == MX_F16) rope_launch<_Float16>(a, layout, grid, st);
+  else if (f == MX_BF16) rope_launch<__bf16>(a, layout, grid, st);
+  else rope_launch<float>(a, layout, grid, st);
   return sync_check(launch_status(), st);
 }
 
@@ -464,16 +517,17 @@ extern "C" int mxkv_append_run(const mxkv_cache* cache, int f, int tokens, const
     if (q->data == q_out->data && (q->token_stride != q_out->token_stride || q->head_stride != q_out->head_stride))
       return MX_ERR_SHAPE;
   }
-  const bool pairs = rope && rope->layout == MXROPE_PAIRS, vec = !rope || vec_ok(rope->layout, rope->rot_dim, 8);
+  const Layout layout = rope ? layout_of(rope->layout, rope->rot_dim, 8) : kHalves;
   AppendArgs a = {};
-  a.k = rope_args(rope, tokens, cache->dim, k, nullptr, positions, 0, 8, vec);
+  a.k = rope_args(rope, tokens, cache->dim, k, nullptr, positions, 0, 8, layout);
   a.k.stream = 4ll * tokens * (cache->heads * 2 + (q ? q->heads : 0)) * cache->dim >= kStreamBytes;
-  tile(a.k, kStage / cache->dim);
+  const int staged = kStageBytes / (2 * cache->dim);  // rows
+  tile(a.k, staged);
   int64_t q_blocks = 0;
   if (q) {
-    a.q = rope_args(rope, tokens, cache->dim, q, q_out, positions, 0, 8, vec);
+    a.q = rope_args(rope, tokens, cache->dim, q, q_out, positions, 0, 8, layout);
     a.q.stream = a.k.stream;
-    tile(a.q, 1 << 20);
+    tile(a.q, layout == kOddHalves ? staged : 1 << 20);
     q_blocks = blocks_of(a.q);
   }
   const int64_t k_blocks = blocks_of(a.k);
@@ -489,7 +543,7 @@ extern "C" int mxkv_append_run(const mxkv_cache* cache, int f, int tokens, const
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
   const dim3 grid((unsigned)(q_blocks + 2 * k_blocks));
-  if (f == MX_F16) append_launch<_Float16>(a, pairs, vec, mx8, grid, st);
-  else append_launch<__bf16>(a, pairs, vec, mx8, grid, st);
+  if (f == MX_F16) append_launch<_Float16>(a, layout, mx8, grid, st);
+  else append_launch<__bf16>(a, layout, mx8, grid, st);
   return sync_check(launch_status(), st);
 }
