@@ -40,7 +40,9 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kTile = 32;                // keys of a wave's tile
 constexpr int kGrain = kTile * kWaves;   // keys that the workgroup's waves take in turn: the unit of work
-constexpr int kFan = 128, kGroup = 64;   // partials that one workgroup joins; groups of more
+// Partials that one workgroup joins, and the groups of more. Small numbers make short code and spread long joins (8
+// rows of up to 47091 keys of one head: 25.8 us with 128 and 64, 20.1 with 32 and 16; 12 x 5 rows: 13.6 and 12.9).
+constexpr int kFan = 32, kGroup = 16;
 constexpr int kDeep = 8;                 // partials that a joining thread has on their way
 constexpr int kPad = 4;                  // floats that keep the heads' rows of the merge on different banks
 // Keys and values are read once: marked non-temporal, they leave the L2 to the program, whose prologue and
@@ -808,6 +810,7 @@ struct Plan {
 // 92 us with one, 100 with two, which double the partials; 64 x 16384 x 8 x 128 E4M3: 372 and 360); fewer where
 // max_len bounds the grains.
 constexpr int kCUs = 256;
+static_assert(2 * kCUs <= kFan * kGroup, "a row's groups are joined in one step");
 // Three counters per workgroup, at one place for every call: a workspace that served another shape has its
 // partials past them.
 constexpr size_t kCounterBytes = 3 * 2 * kCUs * 4;
