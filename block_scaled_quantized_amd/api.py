@@ -286,6 +286,8 @@ class KVCache:
                 continue
             if tuple(t.shape) != (pages, a, b, d) or not t[0].is_contiguous() or (pages > 1 and t.stride(0) * unit != stride):
                 raise MXError(MX_ERR_SHAPE, "KVCache")
+        if any(t.element_size() != (1 if fmt == MX_E4M3 else 2) for t in (k, v)) or any(t.element_size() != 1 for t in (ks, vs) if t is not None):
+            raise MXError(MX_ERR_FORMAT, "KVCache")
         heads, page_size = (a, b) if order == MXKV_HEADS_FIRST else (b, a)
         self.tensors = (k, v, ks, vs)
         self.c = _Cache(fmt, order, pages, page_size, heads, dim, stride, _ptr(k), _ptr(v), _ptr(ks), _ptr(vs))

@@ -8,6 +8,7 @@
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <exception>
 
 #include "mxgemm.h"
@@ -45,12 +46,17 @@ T* address(PyObject* o) {  // of a structure that the caller keeps; None: NULL
   return o == Py_None ? nullptr : reinterpret_cast<T*>((uintptr_t)integer(o));
 }
 
+bool is_int(int64_t n) { return n <= INT_MAX; }
+
 // A [tokens][heads][dim] tensor, dim contiguous. False: another shape.
 bool heads(const at::Tensor& t, mx_heads* h) {
-  if (t.dim() != 3 || (t.stride(2) != 1 && t.size(2) > 1)) return false;
+  if (t.dim() != 3 || (t.stride(2) != 1 && t.size(2) > 1) || !is_int(t.size(0)) || !is_int(t.size(1)) || !is_int(t.size(2))) return false;
   *h = mx_heads{t.data_ptr(), (int)t.size(1), t.stride(0), t.stride(1)};
   return true;
 }
+
+// Whether the tensor's elements have the size of format f's (a wrong one would be read past its end).
+bool fits(const at::Tensor& t, int f) { return t.element_size() == (f == MX_F32 ? 4 : 2); }
 
 // The address of a dense int32 tensor of this shape; None: NULL.
 bool ints(PyObject* o, at::IntArrayRef shape, const int32_t** p) {
@@ -64,7 +70,7 @@ bool ints(PyObject* o, at::IntArrayRef shape, const int32_t** p) {
 
 bool table_of(PyObject* o, mxkv_table* table) {
   const at::Tensor& t = tensor(o);
-  if (t.dim() != 2 || t.scalar_type() != at::kInt || !t.is_contiguous()) return false;
+  if (t.dim() != 2 || t.scalar_type() != at::kInt || !t.is_contiguous() || !is_int(t.size(0)) || !is_int(t.size(1))) return false;
   *table = mxkv_table{static_cast<const int32_t*>(t.data_ptr()), (int)t.size(0), (int)t.size(1)};
   return true;
 }
@@ -104,6 +110,7 @@ int rope(PyObject* const* a) {
   const int32_t* positions;
   if (!heads(x, &hx) || !heads(out, &ho) || x.sizes() != out.sizes() || !ints(a[4], x.sizes().slice(0, 1), &positions)) return MX_ERR_SHAPE;
   const int f = narrow(a[0]), tokens = (int)x.size(0), dim = (int)x.size(2), inverse = narrow(a[5]);
+  if (!fits(x, f) || !fits(out, f)) return MX_ERR_FORMAT;
   const mxrope* r = address<mxrope>(a[1]);
   void* stream = stream_of(a[6]);
   return unlocked([&] { return mxrope_run(f, r, tokens, dim, &hx, &ho, positions, inverse, stream); });
@@ -114,6 +121,7 @@ int append(PyObject* const* a) {
   const mxkv_cache* cache = address<mxkv_cache>(a[0]);
   mx_heads h[4];
   bool given[4];
+  const int f = narrow(a[1]);
   const int64_t n = tensor(a[2]).dim() == 3 ? tensor(a[2]).size(0) : -1;
   const int place[4] = {2, 3, 8, 9};
   for (int i = 0; i < 4; i++) {
@@ -121,11 +129,11 @@ int append(PyObject* const* a) {
     if (!given[i]) continue;
     const at::Tensor& t = tensor(a[place[i]]);
     if (!heads(t, &h[i]) || t.size(0) != n || t.size(2) != cache->dim) return MX_ERR_SHAPE;
+    if (!fits(t, f)) return MX_ERR_FORMAT;
   }
   const int32_t *positions, *seq;
   mxkv_table table;
   if (!table_of(a[5], &table) || !ints(a[4], {n}, &positions) || !ints(a[6], {n}, &seq)) return MX_ERR_SHAPE;
-  const int f = narrow(a[1]);
   const mxrope* r = address<mxrope>(a[7]);
   void* stream = stream_of(a[10]);
   return unlocked([&] {
@@ -159,6 +167,7 @@ int attention(PyObject* const* a) {
   }
   if (a[13] != Py_None) bytes = (size_t)integer(a[13]);
   const int f = narrow(a[1]), max_len = narrow(a[6]);
+  if (!fits(q, f) || !fits(out, f)) return MX_ERR_FORMAT;
   const mxattn_opts opts = {(float)number(a[7]), (float)number(a[11]), narrow(a[10])};
   void* stream = stream_of(a[14]);
   return unlocked([&] {
@@ -171,7 +180,7 @@ int copy(PyObject* const* a) {
   const mxkv_cache* layers = address<mxkv_cache>(a[0]);
   const at::Tensor& t = tensor(a[2]);
   const int32_t* pairs;
-  if (t.dim() != 2 || !ints(a[2], {t.size(0), 2}, &pairs)) return MX_ERR_SHAPE;
+  if (t.dim() != 2 || !is_int(t.size(0)) || !ints(a[2], {t.size(0), 2}, &pairs)) return MX_ERR_SHAPE;
   const int n_layers = narrow(a[1]), n = (int)t.size(0);
   void* stream = stream_of(a[3]);
   return unlocked([&] { return mxkv_copy_run(layers, n_layers, pairs, n, stream); });

@@ -218,6 +218,53 @@ def test_python_refusals():
     assert api.KVCache(api.MX_F16, both[:, 0], both[:, 1]).c.page_stride == 2 * 2 * 16 * 64
 
 
+def test_python_refusals_of_the_cache_calls():
+    """Shapes and element sizes that do not fit are refused before the library is called; what is no tensor is a
+    TypeError."""
+    import torch
+
+    def half(*shape):
+        return torch.zeros(*shape, dtype=torch.float16)
+
+    def ints(*shape):
+        return torch.zeros(*shape, dtype=torch.int32)
+
+    k = half(5, 2, 16, 64)
+    c = api.KVCache(api.MX_F16, k, k)
+    rope = api.Rope(64, P)
+    good = dict(k=half(4, 2, 64), v=half(4, 2, 64), positions=ints(4), table=ints(3, 5), seq=ints(4), rope=rope, q=half(4, 8, 64), q_out=half(4, 8, 64))
+    for bad, status in ((dict(k=half(4, 2, 32)), "SHAPE"), (dict(v=half(3, 2, 64)), "SHAPE"), (dict(q=half(3, 8, 64)), "SHAPE"), (dict(q_out=half(4, 8, 64).transpose(1, 2)), "SHAPE"),
+                        (dict(positions=ints(5)), "SHAPE"), (dict(seq=ints(4).long()), "SHAPE"), (dict(table=ints(3, 5).t()), "SHAPE"), (dict(table=ints(15)), "SHAPE"),
+                        (dict(k=half(4, 2, 64).float()), "FORMAT"), (dict(q_out=half(4, 8, 64).double()), "FORMAT")):
+        kw = dict(good, **bad)
+        with pytest.raises(api.MXError) as e:
+            api.mxkv_append_run(c, api.MX_F16, kw.pop("k"), kw.pop("v"), kw.pop("positions"), kw.pop("table"), stream=0, **kw)
+        assert e.value.status == getattr(api, "MX_ERR_" + status), bad
+    good = dict(q=half(3, 8, 64), out=half(3, 8, 64), table=ints(3, 5), lengths=ints(3), lse=torch.zeros(3, 8), starts=ints(3))
+    for bad, status in ((dict(q=half(3, 8, 32)), "SHAPE"), (dict(out=half(3, 4, 64)), "SHAPE"), (dict(table=ints(4, 5)), "SHAPE"), (dict(lengths=ints(2)), "SHAPE"),
+                        (dict(starts=ints(3).short()), "SHAPE"), (dict(lse=torch.zeros(8, 3).t()), "SHAPE"), (dict(lse=torch.zeros(3, 8).half()), "SHAPE"), (dict(lse=torch.zeros(24)), "SHAPE"),
+                        (dict(q=half(3, 8, 64).float()), "FORMAT"), (dict(out=half(3, 8, 64).float()), "FORMAT")):
+        kw = dict(good, **bad)
+        with pytest.raises(api.MXError) as e:
+            api.mxattn_decode_run(c, api.MX_F16, kw.pop("q"), kw.pop("out"), kw.pop("table"), kw.pop("lengths"), 80, 0.1, stream=0, **kw)
+        assert e.value.status == getattr(api, "MX_ERR_" + status), bad
+    for bad in (ints(4), ints(4, 3), ints(4, 2).long(), ints(2, 4).t()):
+        with pytest.raises(api.MXError) as e:
+            api.mxkv_copy_run([c], bad, stream=0)
+        assert e.value.status == api.MX_ERR_SHAPE
+    for call in (lambda: api.mxrope_run(api.MX_F16, rope, [1.0], half(1, 1, 64), ints(1), stream=0), lambda: api.mxkv_copy_run([c], 7, stream=0),
+                 lambda: api.mxattn_decode_run(c, api.MX_F16, half(3, 8, 64), half(3, 8, 64), ints(3, 5), 3, 80, 0.1, stream=0)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(api.MXError) as e:
+        api.mxrope_run(api.MX_F32, rope, half(4, 8, 64), half(4, 8, 64), ints(4), stream=0)
+    assert e.value.status == api.MX_ERR_FORMAT
+    for args in ((api.MX_F16, k.float(), k.float()), (api.MX_E4M3, k, k, ints(5, 2, 16, 2), ints(5, 2, 16, 2))):
+        with pytest.raises(api.MXError) as e:
+            api.KVCache(*args)
+        assert e.value.status == api.MX_ERR_FORMAT
+
+
 # ---- page pool -----------------------------------------------------------------------------------
 
 class Model:
