@@ -28,6 +28,25 @@ MXMATVEC_SCRATCH_BYTES = 17 << 20  # static scratch of mxmatvec_run_noalloc, per
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m block_scaled_quantized_amd.build`")
 
+
+
+def _load_hip() -> None:
+    """Load torch's own copy of the HIP runtime before the library asks for one. torch needs that copy under a name by which
+    the loader does not find a runtime that is loaded already, so a process that loaded the library first
+    and torch later had two, and the library's saw no device. (Without torch, the system's is loaded.)"""
+    import importlib.util
+    import sys
+    if "torch" in sys.modules:
+        return
+    spec = importlib.util.find_spec("torch")
+    for home in (spec.submodule_search_locations or []) if spec else []:
+        path = os.path.join(home, "lib", "libamdhip64.so")
+        if os.path.exists(path):
+            ctypes.CDLL(path)
+            return
+
+
+_load_hip()
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i, _u, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_int64
 

@@ -265,6 +265,17 @@ def test_python_refusals_of_the_cache_calls():
         assert e.value.status == api.MX_ERR_FORMAT
 
 
+def test_one_hip_runtime_in_a_process():
+    """Whether the package or torch is imported first, both use one copy of the HIP runtime."""
+    import subprocess
+    import sys
+    from conftest import ROOT
+    show = "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))"
+    for first in ("from block_scaled_quantized_amd import api; import torch", "import torch; from block_scaled_quantized_amd import api"):
+        r = subprocess.run([sys.executable, "-c", f"{first}; {show}"], cwd=ROOT, capture_output=True, text=True)
+        assert r.returncode == 0 and r.stdout.split()[-1] == "1", (first, r.stdout, r.stderr)
+
+
 # ---- page pool -----------------------------------------------------------------------------------
 
 class Model:
