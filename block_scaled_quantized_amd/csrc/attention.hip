@@ -248,13 +248,14 @@ MX_DEV float soft_cap(float s, float c) {
 // Tiles of a wave on their way: two, or one of D = 256, whose registers would not hold a second; and one where
 // workgroups take whole units, a few tiles of a wave, whose time is the code's length (8 x 500 keys: 9.4 us, 10.0
 // with two).
-constexpr int tiles_ahead(int D, bool split) { return D == 256 || !split ? 1 : 2; }
-// A query's 32 registers would be spilled of D = 256: a lane keeps them in LDS, where the merge's rows come later.
-constexpr bool query_in_lds(int D) { return D == 256; }
+constexpr int tiles_ahead(int D, bool split, int ht = 1) { return D == 256 || ht > 1 || !split ? 1 : 2; }
+// The queries' 32 registers would be spilled of D = 256 or two head tiles: a lane keeps them in LDS, where the merge's
+// rows come later.
+constexpr bool query_in_lds(int D, int ht) { return D == 256 || ht > 1; }
 // Shares of D = 256 16-bit rows take more than 256 registers (16 x 8192 x 4 fp16: 88 us, spilled into 256 of them
 // 101; E4M3 fits: 64 us against 69), which whole units, small and many, do better without (200 x 4 rows of 30 keys:
 // 15 us against 25). Shares of D = 64 fit three waves (78 x 16 short rows E4M3: 17 us, 20 with two, 24 spilled into four).
-constexpr int waves_per_simd(int D, bool mx8, bool split) { return !split ? 2 : D == 64 ? 3 : D == 256 && !mx8 ? 1 : 2; }
+constexpr int waves_per_simd(int D, bool mx8, bool split, int ht) { return !split || ht > 1 ? 2 : D == 64 ? 3 : D == 256 && !mx8 ? 1 : 2; }
 
 // D: 64, 128 or 256, the head size rounded up. T: type of q, out and the arithmetic. MX8: E4M3 cache.
 // PAGED16: page_size % 16 == 0, so that the 16 keys of half a tile lie in one page: their place is a
@@ -264,23 +265,24 @@ constexpr int waves_per_simd(int D, bool mx8, bool split) { return !split ? 2 : 
 // SPLIT: workgroups take shares of the grains and join what they cut; else one takes a whole unit, and the code
 // of shares and joins, whose instructions would be waited for, is left out (4 x 12 rows of 30 keys: 5.6 us, 6.4
 // with it; eight waves for a unit were slower than four: 8 x 500 keys 11.1 us against 10.0).
-template <int D, typename T, bool MX8, bool PAGED16, bool SPLIT>
-__global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decode_kernel(Args) {
+template <int D, typename T, bool MX8, bool PAGED16, bool SPLIT, int HT>
+__global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void decode_kernel(Args) {
   typedef typename Vec<T>::x8 x8;
   constexpr float kShift = Vec<T>::kShift;
-  constexpr int kGrains = D / 32;          // matrix instructions of one score tile
-  constexpr int kLoads = MX8 ? D / 64 : kGrains;  // 16-byte loads of a key's row
+  constexpr int kSteps = D / 32;          // matrix instructions of one score tile
+  constexpr int kLoads = MX8 ? D / 64 : kSteps;  // 16-byte loads of a key's row
   constexpr int kRuns = D == 256 ? 2 : 1; // runs of kRow elements of V per lane and key
   constexpr int kRow = D == 64 ? 4 : 8;
   constexpr int kOut = D / 16;            // accumulators
   constexpr int kSize = MX8 ? 1 : 2;      // bytes of an element
-  constexpr int kAhead = tiles_ahead(D, SPLIT);
+  constexpr int kAhead = tiles_ahead(D, SPLIT, HT);
+  constexpr int kHeads = 16 * HT;         // query heads of a unit
   constexpr int kBlock = 32;              // tiles of a wave whose pages it looks up at a time
   extern __shared__ float lds[];          // queries: [wave][step][lane]; merge: [kWaves / 2][head][D + kPad]; join: sums, then [head][kFan] weights
-  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16], head_m[16], head_l[16];
+  __shared__ float wave_m[kWaves][kHeads], wave_l[kWaves][kHeads], head_m[kHeads], head_l[kHeads];
   __shared__ int is_last;
-  constexpr bool kQueryInLds = query_in_lds(D);
-  u32x4* const query = reinterpret_cast<u32x4*>(lds) + (threadIdx.x >> 6) * kGrains * 64 + (threadIdx.x & 63);
+  constexpr bool kQueryInLds = query_in_lds(D, HT);
+  u32x4* const query = reinterpret_cast<u32x4*>(lds) + (threadIdx.x >> 6) * HT * kSteps * 64 + (threadIdx.x & 63);
   __shared__ int64_t place_of[PAGED16 ? 1 : kWaves][2][kTile];  // of the keys of a wave's two tiles
 
   Kernarg* const args = (Kernarg*)__builtin_amdgcn_kernarg_segment_ptr();
@@ -302,7 +304,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
     Kernarg& a = *fresh(args);
     const int b = at.b, dim = a.dim;
     const int hk = (int)copy_of(a.tiles_div).div((uint32_t)at.unit), ht = at.unit - hk * a.tiles;
-    const int first_head = hk * a.group + 16 * ht, n_heads = min(16, a.group - 16 * ht);
+    const int first_head = hk * a.group + kHeads * ht, n_heads = min(kHeads, a.group - kHeads * ht);
     const int64_t head_at = (int64_t)hk * a.head_stride, page_stride = a.page_stride, slot_stride = a.slot_stride;
     const int32_t* table = a.table + (int64_t)b * a.cols;
     const FastDiv page_div = copy_of(a.page_div);
@@ -319,21 +321,24 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
     const int length = a.lengths[b], start = (a.starts ? a.starts : a.lengths)[b];
     if (from_zero) page_ahead = page_at(ahead + (PAGED16 ? (lane >> 1) * kGrain + (lane & 1) * 16 : lane & (kTile - 1)));
 
-    // Query fragments: column c, the elements that this lane's K loads hold; zeros past the heads and past dim.
-    x8 qf[kQueryInLds ? 1 : kGrains];
-    {
-      const T* q = (const T*)a.q + (int64_t)b * a.qt + (int64_t)(first_head + (c < n_heads ? c : 0)) * a.qh;
-      u32x4 w[kGrains];
+    // Query fragments: columns c of each head tile, the elements that this lane's K loads hold; zeros past the
+    // heads and past dim.
+    x8 qf[kQueryInLds ? 1 : kSteps];
 #pragma unroll
-      for (int s = 0; s < kGrains; s++) {
+    for (int t = 0; t < HT; t++) {
+      const int head = 16 * t + c;
+      const T* q = (const T*)a.q + (int64_t)b * a.qt + (int64_t)(first_head + (head < n_heads ? head : 0)) * a.qh;
+      u32x4 w[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; s++) {
         const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
         w[s] = *reinterpret_cast<const u32x4*>(q + (d < dim ? d : 0));
       }
 #pragma unroll
-      for (int s = 0; s < kGrains; s++) {
+      for (int s = 0; s < kSteps; s++) {
         const int d = MX8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
-        if (c >= n_heads || d >= dim) w[s] = (u32x4){0u, 0u, 0u, 0u};
-        if constexpr (kQueryInLds) query[64 * s] = w[s];
+        if (head >= n_heads || d >= dim) w[s] = (u32x4){0u, 0u, 0u, 0u};
+        if constexpr (kQueryInLds) query[64 * (t * kSteps + s)] = w[s];
         else qf[s] = __builtin_bit_cast(x8, w[s]);
       }
     }
@@ -359,10 +364,14 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
       }
     const uint8_t *kp = a.k, *vp = a.v, *ksp = a.ks, *vsp = a.vs;
 
-    f32x4 acc[kOut];
+    f32x4 acc[HT][kOut];
+    float m[HT], l[HT];
 #pragma unroll
-    for (int i = 0; i < kOut; i++) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    for (int t = 0; t < HT; t++) {
+#pragma unroll
+      for (int i = 0; i < kOut; i++) acc[t][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      m[t] = -INFINITY, l[t] = 0.f;
+    }
 
     // A tile's K is loaded again as soon as its scores are formed, its V as soon as it is added up.
     struct Tile {
@@ -503,13 +512,18 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
           seen = (z.mask >> (4 * g) & 15u) | (z.mask >> (4 * g + 16) & 15u) << 4;
         }
 
-        // S^T: keys 4 g + i of half h, head c.
-        f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        // S^T: keys 4 g + i of half h, head c of each head tile.
+        f32x4 s[HT][2];
 #pragma unroll
-        for (int st = 0; st < kGrains; st++) {
-          x8 q;
-          if constexpr (kQueryInLds) q = __builtin_bit_cast(x8, query[64 * st]);
-          else q = qf[st];
+        for (int u = 0; u < HT; u++) s[u][0] = s[u][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int st = 0; st < kSteps; st++) {
+          x8 q[HT];
+#pragma unroll
+          for (int u = 0; u < HT; u++) {
+            if constexpr (kQueryInLds) q[u] = __builtin_bit_cast(x8, query[64 * (u * kSteps + st)]);
+            else q[u] = qf[st];
+          }
 #pragma unroll
           for (int h = 0; h < 2; h++) {
             u32x4 w;
@@ -522,43 +536,47 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
             if constexpr (!PAGED16) {
               if ((MX8 ? 64 * (st / 2) + 16 * g : 32 * st + 8 * g) >= dim) w = (u32x4){0u, 0u, 0u, 0u};
             }
-            s[h] = Vec<T>::mfma(__builtin_bit_cast(x8, w), q, s[h]);
+#pragma unroll
+            for (int u = 0; u < HT; u++) s[u][h] = Vec<T>::mfma(__builtin_bit_cast(x8, w), q[u], s[u][h]);
           }
         }
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = s[j / 4][j % 4];
         place_tile(z, it + kAhead);
         load_k(z, it + kAhead);
-        if (softcap > 0.f) {
+        x8 p[HT];
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[j] = kLog2e * soft_cap(x[j] * score_scale, softcap);
-        } else {
+        for (int u = 0; u < HT; u++) {
+          float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[j] *= score_scale * kLog2e;
-        }
-        if (!all_seen) {
+          for (int j = 0; j < 8; j++) x[j] = s[u][j / 4][j % 4];
+          if (softcap > 0.f) {
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[j] = seen >> j & 1u ? x[j] : -INFINITY;
-        }
-        float top = x[0];
+            for (int j = 0; j < 8; j++) x[j] = kLog2e * soft_cap(x[j] * score_scale, softcap);
+          } else {
 #pragma unroll
-        for (int j = 1; j < 8; j++) top = fmaxf(top, x[j]);
-        if (__any(top > m)) {  // seldom after the first tiles
-          top = fmaxf(wave_max(top), m);
-          const float f = __builtin_amdgcn_exp2f(m - finite_or_zero(top));
-          l *= f;
+            for (int j = 0; j < 8; j++) x[j] *= score_scale * kLog2e;
+          }
+          if (!all_seen) {
 #pragma unroll
-          for (int i = 0; i < kOut; i++) acc[i] *= f;
-          m = top;
-        }
-        const float ref = finite_or_zero(m) - kShift;
-        x8 p;
+            for (int j = 0; j < 8; j++) x[j] = seen >> j & 1u ? x[j] : -INFINITY;
+          }
+          float top = x[0];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          const float e = __builtin_amdgcn_exp2f(x[j] - ref);
-          l += e;
-          p[j] = (T)e;
+          for (int j = 1; j < 8; j++) top = fmaxf(top, x[j]);
+          if (__any(top > m[u])) {  // seldom after the first tiles
+            top = fmaxf(wave_max(top), m[u]);
+            const float f = __builtin_amdgcn_exp2f(m[u] - finite_or_zero(top));
+            l[u] *= f;
+#pragma unroll
+            for (int i = 0; i < kOut; i++) acc[u][i] *= f;
+            m[u] = top;
+          }
+          const float ref = finite_or_zero(m[u]) - kShift;
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const float e = __builtin_amdgcn_exp2f(x[j] - ref);
+            l[u] += e;
+            p[u][j] = (T)e;
+          }
         }
 
         // out^T += V^T P^T
@@ -582,7 +600,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
             u32x4 f;
 #pragma unroll
             for (int j = 0; j < 4; j++) f[j] = __builtin_amdgcn_perm(w[2 * j + 1][i / 2], w[2 * j][i / 2], sel);
-            acc[kRow * r + i] = Vec<T>::mfma(__builtin_bit_cast(x8, f), p, acc[kRow * r + i]);
+#pragma unroll
+            for (int u = 0; u < HT; u++)
+              acc[u][kRow * r + i] = Vec<T>::mfma(__builtin_bit_cast(x8, f), p[u], acc[u][kRow * r + i]);
           }
         }
         load_v(z, it + kAhead);
@@ -608,29 +628,39 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
 
     // Merge the waves, referred to their common maximum: half of them put their rows into LDS, the others add
     // theirs, and the readers below add the remaining ones.
-    l = wave_sum(l);
-    if (g == 0) wave_m[wave][c] = m, wave_l[wave][c] = l;
+#pragma unroll
+    for (int u = 0; u < HT; u++) {
+      l[u] = wave_sum(l[u]);
+      if (g == 0) wave_m[wave][16 * u + c] = m[u], wave_l[wave][16 * u + c] = l[u];
+    }
     __syncthreads();
     constexpr int kLd = D + kPad, kHalf = kWaves / 2;
     {
-      float top = wave_m[0][c], sum = 0.f;
+      float f[HT];
 #pragma unroll
-      for (int w = 1; w < kWaves; w++) top = fmaxf(top, wave_m[w][c]);
+      for (int u = 0; u < HT; u++) {
+        const int head = 16 * u + c;
+        float top = wave_m[0][head], sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; w++) sum += wave_l[w][c] * __builtin_amdgcn_exp2f(wave_m[w][c] - finite_or_zero(top));
-      if (wave == 0) head_m[c] = top, head_l[c] = sum;
-      const float f = __builtin_amdgcn_exp2f(m - finite_or_zero(top));
-      float* o = lds + ((wave % kHalf) * n_heads + c) * kLd;
+        for (int w = 1; w < kWaves; w++) top = fmaxf(top, wave_m[w][head]);
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) sum += wave_l[w][head] * __builtin_amdgcn_exp2f(wave_m[w][head] - finite_or_zero(top));
+        if (wave == 0) head_m[head] = top, head_l[head] = sum;
+        f[u] = __builtin_amdgcn_exp2f(m[u] - finite_or_zero(top));
+      }
 #pragma unroll
       for (int round = 1; round >= 0; round--) {
-        if (wave / kHalf == round && c < n_heads) {
+#pragma unroll
+        for (int u = 0; u < HT; u++) {
+          if (wave / kHalf != round || 16 * u + c >= n_heads) continue;
+          float* o = lds + ((wave % kHalf) * n_heads + 16 * u + c) * kLd;
 #pragma unroll
           for (int i = 0; i < kOut; i += 4)
 #pragma unroll
             for (int v = 0; v < 4; v++) {
               // neighbouring accumulators hold neighbouring elements
               f32x4* p = reinterpret_cast<f32x4*>(o + 128 * (i / 8) + kRow * (4 * g + v) + i % kRow);
-              f32x4 w = {acc[i][v] * f, acc[i + 1][v] * f, acc[i + 2][v] * f, acc[i + 3][v] * f};
+              f32x4 w = {acc[u][i][v] * f[u], acc[u][i + 1][v] * f[u], acc[u][i + 2][v] * f[u], acc[u][i + 3][v] * f[u]};
               if (round == 0) w += *p;
               *p = w;
             }
@@ -651,8 +681,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
     };
     const bool whole = !SPLIT || (at.grain == 0 && stop == row.grains);
     // Partials, one for a share that begins within a unit and one for a unit that ends past the share:
-    // [16][dim] outputs, then [16] {maximum, sum}.
-    const uint32_t rows_at = (uint32_t)(16 * dim * 4), slot_size = rows_at + 16 * 8;
+    // [kHeads][dim] outputs, then [kHeads] {maximum, sum}.
+    const uint32_t rows_at = (uint32_t)(kHeads * dim * 4), slot_size = rows_at + kHeads * 8;
     rsrc_t pr;
     if (!whole) pr = __builtin_amdgcn_make_buffer_rsrc(z.partial, (short)0, (int)(2 * z.wgs * slot_size), 0x00020000);
     const int items = n_heads * quads;
@@ -716,31 +746,41 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
           }
         };
         request((int)threadIdx.x - part * items, part);
-        // Weights 2^(m_i - m) of head c and every 4 kWaves-th partial, and the sums
+        // Weights 2^(m_i - m) of the lane's heads and every 4 kWaves-th partial, and the sums
         constexpr int kParts = kFan / (4 * kWaves);
-        float cm[kParts], cl[kParts], top = -INFINITY, sum = 0.f;
+        float cm[HT][kParts], cl[HT][kParts], top[HT];
 #pragma unroll
-        for (int i = 0; i < kParts; i++) {
-          const int ch = 4 * wave + g + 4 * kWaves * i;
-          const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(jr, at0 + ch * stride + (ch == 0 ? extra : 0u) + rows_at + 8 * c, 0, 17));
-          const uint32_t w0 = w[0], w1 = w[1];
-          cm[i] = ch < n && c < n_heads ? bitsf(w0) : -INFINITY, cl[i] = ch < n && c < n_heads ? bitsf(w1) : 0.f;
+        for (int u = 0; u < HT; u++) {
+          const int head = 16 * u + c;
+#pragma unroll
+          for (int i = 0; i < kParts; i++) {
+            const int ch = 4 * wave + g + 4 * kWaves * i;
+            const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(jr, at0 + ch * stride + (ch == 0 ? extra : 0u) + rows_at + 8 * head, 0, 17));
+            const uint32_t w0 = w[0], w1 = w[1];
+            cm[u][i] = ch < n && head < n_heads ? bitsf(w0) : -INFINITY, cl[u][i] = ch < n && head < n_heads ? bitsf(w1) : 0.f;
+          }
+          top[u] = cm[u][0];
+#pragma unroll
+          for (int i = 1; i < kParts; i++) top[u] = fmaxf(top[u], cm[u][i]);
+          top[u] = wave_max(top[u]);
+          wave_m[wave][head] = top[u];
         }
-#pragma unroll
-        for (int i = 0; i < kParts; i++) top = fmaxf(top, cm[i]);
-        top = wave_max(top);
-        wave_m[wave][c] = top;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWaves; w++) top = fmaxf(top, wave_m[w][c]);
+        for (int u = 0; u < HT; u++) {
+          const int head = 16 * u + c;
+          float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kParts; i++) {
-          const float w = __builtin_amdgcn_exp2f(cm[i] - finite_or_zero(top));
-          if (c < n_heads) weight[c * kFan + 4 * wave + g + 4 * kWaves * i] = w;
-          sum += w * cl[i];
+          for (int w = 0; w < kWaves; w++) top[u] = fmaxf(top[u], wave_m[w][head]);
+#pragma unroll
+          for (int i = 0; i < kParts; i++) {
+            const float w = __builtin_amdgcn_exp2f(cm[u][i] - finite_or_zero(top[u]));
+            if (head < n_heads) weight[head * kFan + 4 * wave + g + 4 * kWaves * i] = w;
+            sum += w * cl[u][i];
+          }
+          sum = wave_sum(sum);
+          wave_l[wave][head] = sum;
         }
-        sum = wave_sum(sum);
-        wave_l[wave][c] = sum;
         __syncthreads();
         const auto joined = [&](int h, float& sum) -> float {  // a head's maximum and sum over the partials
           float top = wave_m[0][h];
@@ -793,40 +833,53 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT)) void decod
 // ---- host -----------------------------------------------------------------------------------
 
 // LDS bytes: the merge's rows, the queries, or the join's weights and sums.
-size_t lds_bytes(int D, int n_heads, bool split) {
+size_t lds_bytes(int D, int ht, int n_heads, bool split) {
   const size_t merge = (size_t)(kWaves / 2) * n_heads * (D + kPad) * 4, weights = (size_t)(n_heads * kFan + 4 * kThreads) * 4;
-  const size_t query = query_in_lds(D) ? (size_t)kWaves * D * 32 : 0;
+  const size_t query = query_in_lds(D, ht) ? (size_t)kWaves * D * 32 * ht : 0;
   return std::max(std::max(merge, query), split ? weights : 0);
 }
 
+int padded(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
 struct Plan {
   int64_t units;
-  int tiles, wgs;  // wgs: workgroups that share the grains; 0: no unit is worth splitting
+  int ht, tiles;  // head tiles of 16 of a unit, and units of a cache head
+  int wgs;        // workgroups that share the grains; 0: no unit is worth splitting
   size_t bytes;
 };
 
+constexpr int kCUs = 256;
+static_assert(2 * kCUs <= kFan * kGroup, "a row's groups are joined in one step");
 // The lengths are known on the device only. The grid is one round of workgroups: one to a CU, whose waves
 // have 128 KB on their way, or two where two tiles per wave are less than that (131072 x 8 x 128 fp16:
 // 92 us with one, 100 with two, which double the partials; 64 x 16384 x 8 x 128 E4M3: 372 and 360); fewer where
 // max_len bounds the grains.
-constexpr int kCUs = 256;
-static_assert(2 * kCUs <= kFan * kGroup, "a row's groups are joined in one step");
+int workgroups(int D, int fmt, int ht) {
+  return kCUs * (tiles_ahead(D, true, ht) * kGrain * 2 * D * (fmt == MX_E4M3 ? 1 : 2) < 131072 ? 2 : 1);
+}
+
 // Three counters per workgroup, at one place for every call: a workspace that served another shape has its
 // partials past them.
 constexpr size_t kCounterBytes = 3 * 2 * kCUs * 4;
 
 Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int window) {
   Plan p = {};
-  p.tiles = ceil_div(q_heads / c->heads, 16);
-  p.units = (int64_t)seqs * c->heads * p.tiles;
+  const int D = padded(c->dim), group = q_heads / c->heads;
   // positions from a sequence's first tile: a window may start within it
   const int64_t span = window > 0 && (int64_t)window + kTile < max_len ? (int64_t)window + kTile : max_len;
-  const int64_t grains = ceil_div(span, (int64_t)kGrain), wgs = p.units * grains;
+  const int64_t grains = ceil_div(span, (int64_t)kGrain);
+  // Two head tiles, so that the keys of more than 16 query heads are read once, where that is what the time goes
+  // to: at 16 grains and more of a workgroup (20 heads of 128 bf16, rows of 8192 keys: 94 -> 57 us at 32 grains; of
+  // 32768: 31.0 and 32.5 at 8; of 4096: 20.5 and 28 at 4). D = 256 has no registers for it.
+  const int64_t units = (int64_t)seqs * c->heads * ceil_div(group, 16);
+  p.ht = D < 256 && group > 16 && units * grains >= 16 * workgroups(D, c->fmt, 1) ? 2 : 1;
+  p.tiles = ceil_div(group, 16 * p.ht);
+  p.units = (int64_t)seqs * c->heads * p.tiles;
+  const int64_t wgs = p.units * grains;
   if (grains < kCut || p.units * (grains + 1) >= (int64_t)1 << 30) return p;  // (the device counts in 32 bits)
-  const int D = c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256;
-  const int most = kCUs * (tiles_ahead(D, true) * kGrain * 2 * D * (c->fmt == MX_E4M3 ? 1 : 2) < 131072 ? 2 : 1);
+  const int most = workgroups(D, c->fmt, p.ht);
   p.wgs = (int)(wgs < most ? wgs : most);
-  p.bytes = kCounterBytes + (size_t)(2 * p.wgs) * 16 * (c->dim + 2) * 4;
+  p.bytes = kCounterBytes + (size_t)(2 * p.wgs) * 16 * p.ht * (c->dim + 2) * 4;
   return p;
 }
 
@@ -835,24 +888,27 @@ bool sizes_ok(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
          max_len < 1 << 30 && window >= 0 && (int64_t)seqs * q_heads < (int64_t)1 << 24;
 }
 
-template <int D, typename T, bool MX8, bool SPLIT>
+template <int D, typename T, bool MX8, bool SPLIT, int HT>
 void launch(const Args& a, unsigned wgs, hipStream_t st) {
-  const size_t lds = lds_bytes(D, a.group < 16 ? a.group : 16, SPLIT);
-  if (a.page_size % 16 == 0) hipLaunchKernelGGL((decode_kernel<D, T, MX8, true, SPLIT>), dim3(wgs), dim3(kThreads), lds, st, a);
-  else hipLaunchKernelGGL((decode_kernel<D, T, MX8, false, SPLIT>), dim3(wgs), dim3(kThreads), lds, st, a);
+  const size_t lds = lds_bytes(D, HT, a.group < 16 * HT ? a.group : 16 * HT, SPLIT);
+  if (a.page_size % 16 == 0) hipLaunchKernelGGL((decode_kernel<D, T, MX8, true, SPLIT, HT>), dim3(wgs), dim3(kThreads), lds, st, a);
+  else hipLaunchKernelGGL((decode_kernel<D, T, MX8, false, SPLIT, HT>), dim3(wgs), dim3(kThreads), lds, st, a);
 }
 
-template <int D, typename T, bool MX8>
+template <int D, typename T, bool MX8, int HT>
 void launch_split(const Args& a, const Plan& p, bool split, hipStream_t st) {
-  if (split) launch<D, T, MX8, true>(a, (unsigned)p.wgs, st);
-  else launch<D, T, MX8, false>(a, (unsigned)p.units, st);
+  if (split) launch<D, T, MX8, true, HT>(a, (unsigned)p.wgs, st);
+  else launch<D, T, MX8, false, HT>(a, (unsigned)p.units, st);
 }
 
 template <typename T, bool MX8>
 void launch_dim(const Args& a, const Plan& p, bool split, hipStream_t st) {
-  if (a.dim <= 64) launch_split<64, T, MX8>(a, p, split, st);
-  else if (a.dim <= 128) launch_split<128, T, MX8>(a, p, split, st);
-  else launch_split<256, T, MX8>(a, p, split, st);
+  const int D = padded(a.dim);
+  if (D == 64 && p.ht == 1) launch_split<64, T, MX8, 1>(a, p, split, st);
+  else if (D == 64) launch_split<64, T, MX8, 2>(a, p, split, st);
+  else if (D == 128 && p.ht == 1) launch_split<128, T, MX8, 1>(a, p, split, st);
+  else if (D == 128) launch_split<128, T, MX8, 2>(a, p, split, st);
+  else launch_split<256, T, MX8, 1>(a, p, split, st);
 }
 
 }  // namespace

@@ -388,3 +388,32 @@ def test_attention_empty_rows_among_many():
     for lengths in ([0, 0, 0], [0, 600, 0], [-1, 600, -2 ** 31]):
         out, lse = run(api, c, "f16", q, table, lengths, 960)
         check(c, "f16", q, out, lse, table, lengths)
+
+
+@pytest.mark.parametrize("kind,cache,hq,hk,dim,page,seqs,n", [
+    ("f16", "f16", 40, 2, 128, 16, 4, 66000), ("bf16", "e4m3", 132, 4, 64, 64, 60, 4400), ("f16", "e4m3", 34, 1, 96, 24, 9, 120000),
+    ("bf16", "bf16", 17, 1, 8, 5, 40, 13200), ("f16", "f16", 20, 1, 128, 32, 2400, 250)])
+@pytest.mark.parametrize("split", [True, False])
+def test_attention_many_heads_to_a_cache_head(kind, cache, hq, hk, dim, page, seqs, n, split):
+    """More than 16 query heads per cache head, with enough keys that two tiles of heads meet a key together. Sequences share
+    one table row, so that the 64-bit form takes each of their few lengths once."""
+    api = require_gpu()
+    say(f"attention {cache}: {hq}/{hk} heads of {dim}, {seqs} rows of up to {n}, split={split}")
+    if not split and n > 60000:
+        seqs = 2
+    pages = -(-n // page) + 1
+    c = Cache(cache, "heads", pages, page, hk, dim, 8)
+    table = np.repeat(tables([n], page, pages, 3), seqs, 0)
+    some = [n, n - 129, n // 3, 0, 1]
+    lengths = [some[i % 5] if i % 7 == 0 else n for i in range(seqs)]
+    q = normal((5, hq, dim), kind, 5)[torch.arange(seqs, device="cuda") % 5]
+    out, lse = run(api, c, kind, q, table, lengths, n, split=split)
+    firsts = {}
+    for i in range(seqs):
+        firsts.setdefault((i % 5, lengths[i]), i)
+    pick = sorted(firsts.values())[:6]
+    check(c, kind, q[pick], out[pick], lse[pick], table[pick], [lengths[i] for i in pick])
+    for i in range(seqs):                                   # equal rows, wherever they lie in the batch
+        j = firsts[i % 5, lengths[i]]
+        tol = 4 * ref.HALF_STEP[kind]
+        assert torch.allclose(out[i].float(), out[j].float(), rtol=tol, atol=tol), i
