@@ -239,10 +239,13 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
   return per;
 }
 
-// c tanh(s / c) by one exponential: its error is relative to c, which is what a score's counts for.
+// c tanh(s / c): where |s / c| < 0.2 by its series, whose fifth term is below half a step, else by one
+// exponential, whose error is relative to c. A cap that is far above every score leaves them as they are.
 MX_DEV float soft_cap(float s, float c) {
-  const float e = __builtin_amdgcn_exp2f(s * fminf(2.0f * kLog2e / c, 3.0e38f));
-  return c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
+  const float y = s * fminf(1.0f / c, 3.0e38f), z = y * y;
+  const float near = s * fmaf(z, fmaf(z, fmaf(z, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
+  const float far = fmaf(c, -2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.0f * kLog2e * y)), c);
+  return fabsf(y) < 0.2f ? near : far;
 }
 
 // Tiles of a wave on their way: two, or one of D = 256, whose registers would not hold a second; and one where

@@ -417,3 +417,16 @@ def test_attention_many_heads_to_a_cache_head(kind, cache, hq, hk, dim, page, se
         j = firsts[i % 5, lengths[i]]
         tol = 4 * ref.HALF_STEP[kind]
         assert torch.allclose(out[i].float(), out[j].float(), rtol=tol, atol=tol), i
+
+
+@pytest.mark.parametrize("softcap", [1e6, 1e30, 3e38])
+def test_attention_cap_far_above_the_scores(softcap):
+    """s^3 / (3 c^2), what such a cap takes off a score of up to 100, is below a half step of it, so the
+    bound without a cap holds."""
+    api = require_gpu()
+    say(f"attention softcap={softcap}")
+    c = Cache("bf16", "heads", 12, 16, 2, 64, 4)
+    table = tables([190], 16, 12, 3)
+    q = normal((1, 4, 64), "bf16", 5, sigma=3.0)
+    out, lse = run(api, c, "bf16", q, table, [190], 190, softcap=softcap)
+    check(c, "bf16", q, out, lse, table, [190])
