@@ -227,6 +227,7 @@ struct RopeArgs {
   void* out;
   int64_t xt, xh, ot, oh;
   int tokens, heads, tile_t, tile_h, groups;  // groups: runs of tile_h heads
+  FastDiv groups_div;
   Split split;
   bool stream;
 };
@@ -234,7 +235,7 @@ struct RopeArgs {
 template <typename T, Layout L, bool STREAM>
 MX_DEV void rope_block(const RopeArgs& a, int block, float2* trig, T* stage) {
   constexpr int U = Unit<T>::N;
-  const int g = block % a.groups, t0 = (block / a.groups) * a.tile_t, h0 = g * a.tile_h;
+  const int tile = (int)a.groups_div.div(block), g = block - tile * a.groups, t0 = tile * a.tile_t, h0 = g * a.tile_h;
   const Rows<T> z = {(const T*)a.x, a.xt, a.xh, t0, min(a.tile_t, a.tokens - t0), h0, min(a.tile_h, a.heads - h0)};
   const auto out = [&](int t, int h) -> T* { return (T*)a.out + (int64_t)(t0 + t) * a.ot + (int64_t)(h0 + h) * a.oh; };
   if constexpr (L != kOddHalves) {
@@ -343,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, bool mx8
   block -= a.q_blocks;
   const bool key = block < a.k_blocks;
   if (!key) block -= a.k_blocks;
-  const int g = block % a.k.groups, t0 = (block / a.k.groups) * a.k.tile_t, h0 = g * a.k.tile_h;
+  const int tile = (int)a.k.groups_div.div(block), g = block - tile * a.k.groups, t0 = tile * a.k.tile_t, h0 = g * a.k.tile_h;
   const int tokens = min(a.k.tile_t, a.k.tokens - t0), heads = min(a.k.tile_h, a.k.heads - h0);
   fill_slots(a, t0, tokens, slot);
   if (key && a.turn) {
@@ -401,6 +402,7 @@ void tile(RopeArgs& a, int max_rows) {
   // few tokens: spread a token's heads over workgroups instead
   while (a.tile_t == 1 && a.tile_h > per && (int64_t)a.tokens * ceil_div(a.heads, a.tile_h) < 512) a.tile_h = ceil_div(a.tile_h, 2);
   a.groups = ceil_div(a.heads, a.tile_h);
+  a.groups_div = FastDiv((uint32_t)a.groups);
 }
 
 int64_t blocks_of(const RopeArgs& a) { return (int64_t)ceil_div(a.tokens, a.tile_t) * a.groups; }
