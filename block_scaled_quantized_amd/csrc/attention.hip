@@ -60,7 +60,7 @@ struct Args {
   uint32_t* counters;
   float* partial;
   int64_t qt, qh, ot, oh, page_stride, head_stride, slot_stride;
-  int seqs, heads, group, tiles, dim, cols, pages, page_size, max_len, max_keys, window, wgs, entry;
+  int seqs, heads, group, tiles, dim, cols, pages, page_size, max_len, max_keys, window, wgs;
   float scale, softcap;
   FastDiv page_div, units_div, tiles_div, wgs_div, quads_div;  // units: of one sequence
 };
@@ -174,8 +174,7 @@ MX_DEV uint32_t wave_scan(uint32_t x) {
   return x;
 }
 
-// A place in the list of all units' grains: sequence, unit within it, grain. In the list each unit's grains
-// follow `entry` that stand for its beginning and end; `at` is the sequence's place in it.
+// A place in the list of all units' grains: sequence, unit within it, grain; `at` is the sequence's place in the list.
 struct Place {
   int b, unit, grain;
   uint32_t at;
@@ -189,17 +188,36 @@ struct Place {
 constexpr int kCut = 5;
 MX_DEV int least_of(uint32_t per, int grains) { return grains < kCut ? grains : (int)min(max(per / 2u, 1u), 4u); }
 
-// This workgroup's share of the grains, from..to, of equal size (which is returned) but for the cuts'
-// distance from the units' ends. Every wave sums up the lengths by itself, a sequence to a lane: a handful
-// of loads that all find in the caches, where a launch that planned would cost its own latency, and no
-// barrier. (Short code counts here: a workgroup runs it once, and its instructions come from memory.)
-MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
+// The list of `all` places is cut into equal shares: cut i is at ceil(i all / wgs) (rounded up, so that units of one
+// length are cut as if their beginnings did not count), of at least `per` places each. Where a share has more than a
+// grain, `entry` = 1: each unit's grains follow one place for its beginning and end, which cost about as much (128
+// ragged rows of up to 1000 keys: 20.5 -> 14.9 us; 32 x 8 of up to 8192: 60.4 -> 54.4; 12 x 5 rows in 512 shares:
+// 13.7 us with it, 13.0 without).
+struct Cuts {
+  uint32_t all, per, wgs, entry;  // wgs: at most one per place
+};
+MX_DEV uint32_t cut_at(const Cuts& c, const FastDiv& wgs_div, uint32_t i) {
+  return i >= c.wgs ? c.all : i * c.per + wgs_div.div(i * (c.all - c.per * c.wgs) + c.wgs - 1u);
+}
+// The last cut at or before place x: x wgs / all, by a product's guess, which is off by one at most.
+MX_DEV int cut_before(const Cuts& c, uint32_t x) {
+  const int q = uniform((int)((float)x * (float)c.wgs * __builtin_amdgcn_rcpf((float)c.all)));
+  const int64_t left = (int64_t)x * c.wgs - (int64_t)q * c.all;
+  return q + (left >= c.all ? 1 : 0) - (left < 0 ? 1 : 0);
+}
+
+// This workgroup's share of the grains, from..to, equal but for the cuts' distance from the units' ends. Every
+// wave sums up the lengths by itself, a sequence to a lane: a handful of loads that all find in the caches,
+// where a launch that planned would cost its own latency, and no barrier. (Short code counts here: a
+// workgroup runs it once, and its instructions come from memory.)
+MX_DEV Cuts share_of(Kernarg& a, int units, Place& from, Place& to) {
   const int lane = threadIdx.x & 63;
+  Cuts cuts = {};
   uint32_t size, before, total;
   const int32_t *lengths = a.lengths, *starts = a.starts ? a.starts : lengths;
   const auto look = [&](int b0) {
     const int b = min(b0 + lane, a.seqs - 1), length = lengths[b], start = starts[b];
-    size = (uint32_t)row_of(a, length, a.starts ? start : 0).grains + a.entry;
+    size = (uint32_t)row_of(a, length, a.starts ? start : 0).grains + cuts.entry;
     if (b0 + lane >= a.seqs) size = 0u;
     before = wave_scan(size);
     total = (uint32_t)__builtin_amdgcn_readlane((int)before, 63);
@@ -211,23 +229,28 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
     look(b0);
     all += total;
   }
-  all *= (uint32_t)units;  // below 2^31
-  const uint32_t per = copy_of(a.wgs_div).div(all + (uint32_t)a.wgs - 1u);
+  all *= (uint32_t)units;
+  if (all > (uint32_t)a.wgs) {
+    cuts.entry = 1u, all += (uint32_t)(a.seqs * units);  // below 2^31
+    if (a.seqs <= 64) size += lane < a.seqs ? 1u : 0u, before += (uint32_t)min(lane, a.seqs), total += (uint32_t)a.seqs;
+  }
+  cuts.all = all, cuts.per = copy_of(a.wgs_div).div(all), cuts.wgs = (uint32_t)a.wgs;
+  if (cuts.per == 0u) cuts.per = 1u, cuts.wgs = all;
   uint32_t sum = 0u;
   from = to = Place{a.seqs, 0, 0, all};
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
     if (a.seqs > 64) look(b0);
 #pragma unroll 1
     for (int side = 0; side < 2; side++) {
-      const uint32_t cut = min(all, (blockIdx.x + side) * per);
+      const uint32_t cut = cut_at(cuts, copy_of(a.wgs_div), blockIdx.x + side);
       const uint32_t q = copy_of(a.units_div).div(cut) - sum;  // grains of a unit's column before the cut's
       if (cut >= all || q >= total) continue;  // (a cut before this block wraps around)
       const int at_lane = 63 - __builtin_clzll(__ballot(before <= q));  // the last one that starts at or before q
       const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)size, at_lane);
       Place p = {b0 + at_lane, 0, 0, (sum + (uint32_t)__builtin_amdgcn_readlane((int)before, at_lane)) * units};
       p.unit = uniform((int)((cut - p.at) / n));
-      const int grains = (int)n - a.entry, least = least_of(per, grains);
-      p.grain = (int)(cut - p.at - p.unit * n) - a.entry;
+      const int grains = (int)(n - cuts.entry), least = least_of(cuts.per, grains);
+      p.grain = (int)(cut - p.at - p.unit * n - cuts.entry);
       if (p.grain < least) p.grain = 0;
       else if (grains - p.grain < least) p.grain = 0, p.unit++;
       if (p.unit == units) p = Place{p.b + 1, 0, 0, p.at + n * units};
@@ -236,7 +259,7 @@ MX_DEV uint32_t share_of(Kernarg& a, int units, Place& from, Place& to) {
     }
     sum += total;
   }
-  return per;
+  return cuts;
 }
 
 // c tanh(s / c): where |s / c| < 0.2 by its series, whose fifth term is below half a step, else by one
@@ -292,9 +315,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   const int units = args->heads * args->tiles;
   Place at, end = {};
-  uint32_t per = 1u;
+  Cuts cuts = {};
   if constexpr (SPLIT) {
-    per = share_of(*args, units, at, end);
+    cuts = share_of(*args, units, at, end);
   } else {
     const int b = (int)copy_of(args->units_div).div(blockIdx.x);
     at = Place{b, (int)blockIdx.x - b * units, 0, 0};
@@ -712,9 +735,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
     // memory, as each workgroup runs it once.
     if constexpr (!SPLIT) break;
     if (!whole) {
-      const uint32_t u0 = at.at + (uint32_t)(at.unit * (row.grains + z.entry) + z.entry), least = least_of(per, row.grains);
-      const int first = uniform((int)((u0 + least + per - 1) / per)) - 1;  // the unit's first workgroup
-      const int members = uniform((int)((u0 + row.grains - least) / per)) - first + 1;
+      const uint32_t u0 = at.at + (uint32_t)at.unit * (row.grains + cuts.entry) + cuts.entry, least = least_of(cuts.per, row.grains);
+      const int first = cut_before(cuts, u0 + least - 1u);  // the unit's first workgroup
+      const int members = cut_before(cuts, u0 + row.grains - least) - first + 1;
       const int groups = members <= kFan ? 1 : ceil_div(members, kGroup), group = groups == 1 ? 0 : ((int)blockIdx.x - first) / kGroup;
       float* share = lds;                  // sums of a head's runs of partials, below
       float* weight = lds + 4 * kThreads;  // [head][kFan]
@@ -829,7 +852,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
 
     at.grain = 0;
     if (stop < row.grains) break;
-    if (++at.unit == units) at = Place{b + 1, 0, 0, at.at + (uint32_t)((row.grains + fresh(args)->entry) * units)};
+    if (++at.unit == units) at = Place{b + 1, 0, 0, at.at + (row.grains + cuts.entry) * units};
   }
 }
 
@@ -947,10 +970,6 @@ extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads*
   a.table = table->pages, a.cols = table->cols, a.lengths = lengths, a.starts = starts;
   const bool split = p.wgs > 0 && workspace && workspace_bytes >= p.bytes;  // else a workgroup takes a whole unit
   a.wgs = p.wgs;
-  // Beginning and ending a unit counts as a grain in the shares where they hold units by the handful (128 ragged
-  // rows of up to 1000 keys: 20.9 -> 14.5 us; 32 x 8 of up to 8192: 59.6 -> 53.9), not where a few long rows then
-  // would end off the shares' borders (8 x 131072 keys: 87.9 -> 91.5 us).
-  a.entry = 4 * p.units >= p.wgs ? 1 : 0;
   if (split) {
     a.counters = (uint32_t*)workspace;
     a.partial = (float*)((uint8_t*)workspace + kCounterBytes);
