@@ -189,21 +189,25 @@ constexpr int kCut = 5;
 MX_DEV int least_of(uint32_t per, int grains) { return grains < kCut ? grains : (int)min(max(per / 2u, 1u), 4u); }
 
 // The list of `all` places is cut into equal shares: cut i is at ceil(i all / wgs) (rounded up, so that units of one
-// length are cut as if their beginnings did not count), of at least `per` places each. Where a share has more than a
-// grain, `entry` = 1: each unit's grains follow one place for its beginning and end, which cost about as much (128
-// ragged rows of up to 1000 keys: 20.5 -> 14.9 us; 32 x 8 of up to 8192: 60.4 -> 54.4; 12 x 5 rows in 512 shares:
-// 13.7 us with it, 13.0 without).
+// length are cut as if their beginnings did not count). Shares of one to four places are rounded up to whole ones
+// where that makes them a quarter longer at most, as fewer cuts then count for more (64 x 8 ragged rows of up to 1000
+// keys E4M3: 20.7 us, 23.2 cut evenly; 16 x 8 of up to 2000: 18.7 and 19.8; where it makes them longer, the
+// even cuts win: 12 x 5 rows of up to 4000, 2.1 places: 17.9 us, 21.3 rounded up; and so they do above four: 16 x 4 of
+// 2000, 4.25 places: 19.2 and 22.1). Where a share has more than a grain, `entry` = 1: each unit's grains follow one
+// place for its beginning and end, which cost about as much (128 ragged rows of up to 1000 keys: 20.5 -> 14.9 us;
+// 32 x 8 of up to 8192: 60.4 -> 54.4; 12 x 5 rows in 512 shares: 13.7 us with it, 13.0 without).
 struct Cuts {
-  uint32_t all, per, wgs, entry;  // wgs: at most one per place
+  uint32_t all, per, rest, entry;  // rest: places that even shares of `per` leave
+  uint32_t num, den;               // cuts per place
 };
-MX_DEV uint32_t cut_at(const Cuts& c, const FastDiv& wgs_div, uint32_t i) {
-  return i >= c.wgs ? c.all : i * c.per + wgs_div.div(i * (c.all - c.per * c.wgs) + c.wgs - 1u);
+MX_DEV uint32_t cut_at(const Cuts& c, Kernarg& a, uint32_t i) {
+  return min(c.all, i * c.per + copy_of(a.wgs_div).div(i * c.rest + (uint32_t)a.wgs - 1u));
 }
-// The last cut at or before place x: x wgs / all, by a product's guess, which is off by one at most.
+// The last cut at or before place x, x num / den, by a product's guess, which is off by one at most.
 MX_DEV int cut_before(const Cuts& c, uint32_t x) {
-  const int q = uniform((int)((float)x * (float)c.wgs * __builtin_amdgcn_rcpf((float)c.all)));
-  const int64_t left = (int64_t)x * c.wgs - (int64_t)q * c.all;
-  return q + (left >= c.all ? 1 : 0) - (left < 0 ? 1 : 0);
+  const int q = uniform((int)((float)x * (float)c.num * __builtin_amdgcn_rcpf((float)c.den)));
+  const int64_t left = (int64_t)x * c.num - (int64_t)q * c.den;
+  return q + (left >= c.den ? 1 : 0) - (left < 0 ? 1 : 0);
 }
 
 // This workgroup's share of the grains, from..to, equal but for the cuts' distance from the units' ends. Every
@@ -234,15 +238,19 @@ MX_DEV Cuts share_of(Kernarg& a, int units, Place& from, Place& to) {
     cuts.entry = 1u, all += (uint32_t)(a.seqs * units);  // below 2^31
     if (a.seqs <= 64) size += lane < a.seqs ? 1u : 0u, before += (uint32_t)min(lane, a.seqs), total += (uint32_t)a.seqs;
   }
-  cuts.all = all, cuts.per = copy_of(a.wgs_div).div(all), cuts.wgs = (uint32_t)a.wgs;
-  if (cuts.per == 0u) cuts.per = 1u, cuts.wgs = all;
+  cuts.all = all, cuts.per = copy_of(a.wgs_div).div(all);
+  cuts.rest = all - cuts.per * (uint32_t)a.wgs, cuts.num = (uint32_t)a.wgs, cuts.den = all;
+  if (cuts.per == 0u || (cuts.per < 4u && 4u * ((uint32_t)a.wgs - cuts.rest) <= all)) {
+    cuts.per += cuts.rest ? 1u : 0u;
+    cuts.rest = 0u, cuts.num = 1u, cuts.den = cuts.per;
+  }
   uint32_t sum = 0u;
   from = to = Place{a.seqs, 0, 0, all};
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
     if (a.seqs > 64) look(b0);
 #pragma unroll 1
     for (int side = 0; side < 2; side++) {
-      const uint32_t cut = cut_at(cuts, copy_of(a.wgs_div), blockIdx.x + side);
+      const uint32_t cut = cut_at(cuts, a, blockIdx.x + side);
       const uint32_t q = copy_of(a.units_div).div(cut) - sum;  // grains of a unit's column before the cut's
       if (cut >= all || q >= total) continue;  // (a cut before this block wraps around)
       const int at_lane = 63 - __builtin_clzll(__ballot(before <= q));  // the last one that starts at or before q
