@@ -430,3 +430,18 @@ def test_attention_cap_far_above_the_scores(softcap):
     q = normal((1, 4, 64), "bf16", 5, sigma=3.0)
     out, lse = run(api, c, "bf16", q, table, [190], 190, softcap=softcap)
     check(c, "bf16", q, out, lse, table, [190])
+
+
+@pytest.mark.parametrize("seqs,n", [(64, 2000), (128, 500), (70, 1400)])
+def test_attention_rows_of_one_length(seqs, n):
+    """Equal rows, whose shares' cuts lie at fractions of a grain: fewer and more sequences than a wave sums up at a
+    time, shares of one place to several."""
+    api = require_gpu()
+    say(f"attention: {seqs} rows of {n}")
+    lengths = [n] * seqs
+    pages = seqs * (-(-n // 64))
+    c = Cache("f16", "heads", pages, 64, 2, 64, 9)
+    table = tables(lengths, 64, pages, 3)
+    q = normal((seqs, 4, 64), "f16", 5)
+    out, lse = run(api, c, "f16", q, table, lengths, n)
+    check(c, "f16", q, out, lse, table, lengths)
