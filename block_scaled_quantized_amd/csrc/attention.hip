@@ -70,10 +70,14 @@ struct Vec;
 template <>
 struct Vec<_Float16> {
   typedef f16x8 x8;
-  // Probabilities are rounded to T for the matrix cores. p = 2^(x - m) is at most 1; binary16 would lose
-  // those under 2^-24, which can matter in number in a long row, so they are scaled by 2^15 (which
-  // cancels in the division by their sum). bfloat16 has the range.
-  static constexpr float kShift = 15.0f;
+  // A probability p = 2^(x - m) goes to the matrix cores as two values of T: p cut to T, and what that leaves rounded
+  // to T. Together they hold 21 bits of p (bfloat16: 15). One value alone made the error against 64 bits 1.2 to 1.4
+  // times that of the result's own rounding. The second is never 0 nor negative, as its product with an infinite value has
+  // to be what the first one's is: kLeast, 2^-39 of the largest p (bfloat16: 2^-126), is far below a half step of any sum.
+  // p is at most 1; binary16 would lose those under 2^-24, which can matter in number in a long row, so they
+  // are scaled by 2^15 (which cancels in the division by their sum). bfloat16 has the range.
+  static constexpr float kShift = 15.0f, kLeast = 0x1p-24f;
+  static MX_DEV uint32_t cut(float a, float b) { return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b)); }
   static MX_DEV f32x4 mfma(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
   template <bool HI>
   static MX_DEV uint32_t from_e4m3(uint32_t w, float scale) {
@@ -83,7 +87,8 @@ struct Vec<_Float16> {
 template <>
 struct Vec<__bf16> {
   typedef bf16x8 x8;
-  static constexpr float kShift = 0.0f;
+  static constexpr float kShift = 0.0f, kLeast = 0x1p-126f;
+  static MX_DEV uint32_t cut(float a, float b) { return __builtin_amdgcn_perm(fbits(b), fbits(a), 0x07060302u); }
   static MX_DEV f32x4 mfma(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
   template <bool HI>
   static MX_DEV uint32_t from_e4m3(uint32_t w, float scale) {
@@ -576,7 +581,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
         }
         place_tile(z, it + kAhead);
         load_k(z, it + kAhead);
-        x8 p[HT];
+        x8 p[HT], rest[HT];
 #pragma unroll
         for (int u = 0; u < HT; u++) {
           float x[8];
@@ -607,10 +612,12 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
           const float ref = finite_or_zero(m[u]) - kShift;
 #pragma unroll
           for (int j = 0; j < 8; j++) {
-            const float e = __builtin_amdgcn_exp2f(x[j] - ref);
-            l[u] += e;
-            p[u][j] = (T)e;
+            x[j] = __builtin_amdgcn_exp2f(x[j] - ref);
+            l[u] += x[j];
           }
+          p[u] = __builtin_bit_cast(x8, (u32x4){Vec<T>::cut(x[0], x[1]), Vec<T>::cut(x[2], x[3]), Vec<T>::cut(x[4], x[5]), Vec<T>::cut(x[6], x[7])});
+#pragma unroll
+          for (int j = 0; j < 8; j++) rest[u][j] = (T)fmaxf(x[j] - (float)p[u][j], Vec<T>::kLeast);
         }
 
         // out^T += V^T P^T
@@ -635,8 +642,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
 #pragma unroll
             for (int j = 0; j < 4; j++) f[j] = __builtin_amdgcn_perm(w[2 * j + 1][i / 2], w[2 * j][i / 2], sel);
 #pragma unroll
-            for (int u = 0; u < HT; u++)
-              acc[u][kRow * r + i] = Vec<T>::mfma(__builtin_bit_cast(x8, f), p[u], acc[u][kRow * r + i]);
+            for (int u = 0; u < HT; u++) {
+              f32x4& o = acc[u][kRow * r + i];
+              o = Vec<T>::mfma(__builtin_bit_cast(x8, f), rest[u], o);
+              o = Vec<T>::mfma(__builtin_bit_cast(x8, f), p[u], o);
+            }
           }
         }
         load_v(z, it + kAhead);

@@ -403,9 +403,10 @@ typedef struct {
  *    [seqs][q heads], may be NULL.
  *  - Positions outside the range are never used, whatever their slots hold (NaN included). lengths
  *    above max_len, or above cols * page_size, are taken as that bound; negative ones as 0.
- *  - Scores, statistics and sums are fp32; the probabilities are rounded to 16 bits for the matrix
- *    cores. E4M3 elements are scaled into f's format (exact in bfloat16; in binary16 where the value
- *    is in its range, as every value that mxkv_append_run wrote from binary16 is).
+ *  - Scores, statistics and sums are fp32; a probability goes to the matrix cores as two 16-bit values,
+ *    which hold 21 bits of it for MX_F16 and 15 for MX_BF16. E4M3 elements are scaled into f's format (exact
+ *    in bfloat16; in binary16 where the value is in its range, as every value that mxkv_append_run wrote
+ *    from binary16 is).
  * Workspace, as for mxmatvec_run: the rows' keys are shared evenly among workgroups, and where a share
  * cuts a row, partial results and counters live in a caller-owned device buffer of
  * mxattn_decode_workspace_size() bytes, zero-filled before its first use and left reusable by every
