@@ -18,7 +18,8 @@ struct mxkv_pool_state {
   std::priority_queue<int32_t, std::vector<int32_t>, std::greater<int32_t>> free;
 
   int32_t* row(int s) { return table.data() + (size_t)s * cols; }
-  int held(int s) const { return (lengths[s] + page_size - 1) / page_size; }
+  int pages_of(int tokens) const { return (int)(((int64_t)tokens + page_size - 1) / page_size); }  // the sum can pass 2^31
+  int held(int s) const { return pages_of(lengths[s]); }
   int32_t take() {
     const int32_t p = free.top();
     free.pop();
@@ -88,7 +89,7 @@ int mxkv_pool_destroy(mxkv_pool p) {
 int mxkv_pool_resize(mxkv_pool p, int seq, int tokens, int32_t pair[2], int* n_pairs) {
   if (!p || !pair || !n_pairs) return MX_ERR_NULL;
   if (!has(p, seq) || tokens < 0 || tokens > (int64_t)p->cols * p->page_size) return MX_ERR_SHAPE;
-  const int had = p->held(seq), need = (int)(((int64_t)tokens + p->page_size - 1) / p->page_size);
+  const int had = p->held(seq), need = p->pages_of(tokens);
   int32_t* row = p->row(seq);
   const bool grows = tokens > p->lengths[seq];
   const bool own = grows && p->lengths[seq] % p->page_size != 0 && p->holders[row[had - 1]] > 1;
@@ -127,7 +128,7 @@ int mxkv_pool_reorder(mxkv_pool p, const int32_t* from) {
     if (!has(p, from[s])) return MX_ERR_SHAPE;
   return guarded([&] {
     const std::vector<int32_t> table = p->table, lengths = p->lengths;  // may throw: nothing has changed yet
-    const auto held = [&](int s) { return (lengths[s] + p->page_size - 1) / p->page_size; };
+    const auto held = [&](int s) { return p->pages_of(lengths[s]); };
     for (int s = 0; s < p->seqs; s++)  // the new holders first, so that no page that stays is given up
       for (int c = 0; c < held(from[s]); c++) p->holders[table[(size_t)from[s] * p->cols + c]]++;
     for (int s = 0; s < p->seqs; s++) {

@@ -387,3 +387,23 @@ def test_pool_refusals():
     assert lib.mxkv_pool_compact(pool.handle, pair, -1, ctypes.byref(n)) == api.MX_ERR_SHAPE
     assert lib.mxkv_pool_fork(None, 0, 1) == lib.mxkv_pool_reorder(None, pair) == api.MX_ERR_NULL
     assert lib.mxkv_pool_table(None) is None and lib.mxkv_pool_used(None) == 0 and lib.mxkv_pool_destroy(None) == api.MX_OK
+
+
+def test_pool_lengths_near_two_to_the_31():
+    """A length whose last page ends past 2^31 - 1 when rounded up: its pages are given back, shared and reordered."""
+    page, cols = 2049, 1048064
+    top = cols * page
+    assert top < 2 ** 31 <= top + page - 1
+    pool = api.KVPool(cols, page, 2, cols)
+    assert pool.resize(0, top) == [] and pool.used == cols
+    assert pool.resize(0, 0) == [] and pool.used == 0
+    pool.resize(0, top)
+    pool.fork(0, 1)
+    pool.reorder([1, 1])
+    assert pool.used == cols and pool.lengths().tolist() == [top, top] and (pool.table()[1] == pool.table()[0]).all()
+    assert pool.compact(4) == []
+    pool.resize(0, 0)
+    assert pool.used == cols
+    pool.resize(1, 0)
+    assert pool.used == 0 and (pool.table() == -1).all()
+    pool.close()
