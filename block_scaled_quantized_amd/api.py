@@ -256,9 +256,14 @@ def int_shapes(fw: int, K: int, N: int):
 # ---- the decode step's cache: rotary positions, append, attention, pages ------------------------
 
 class Rope:
-    """An mxrope: freq is a device tensor of rot_dim / 2 doubles, which is kept alive here."""
+    """An mxrope: freq is a device tensor of rot_dim / 2 doubles (or more), which is kept alive here, or an address."""
 
     def __init__(self, rot_dim: int, freq, layout: int = MXROPE_HALF, factor: float = 1.0):
+        if hasattr(freq, "data_ptr"):
+            if not freq.dtype.is_floating_point or freq.element_size() != 8:
+                raise MXError(MX_ERR_FORMAT, "Rope")
+            if not freq.is_contiguous() or freq.numel() < rot_dim // 2:
+                raise MXError(MX_ERR_SHAPE, "Rope")
         self.freq = freq
         self.c = _Rope(rot_dim, layout, _ptr(freq), factor)
         self.ref = ctypes.addressof(self.c)

@@ -407,3 +407,16 @@ def test_pool_lengths_near_two_to_the_31():
     pool.resize(1, 0)
     assert pool.used == 0 and (pool.table() == -1).all()
     pool.close()
+
+
+def test_rope_refuses_frequencies_that_are_not_rot_dim_halves_of_doubles():
+    """The kernels read rot_dim / 2 doubles at the tensor's address."""
+    import torch
+    f = torch.zeros(64, dtype=torch.float64)
+    for bad, status in ((f.float(), "FORMAT"), (f.long(), "FORMAT"), (f.half(), "FORMAT"), (f[:63], "SHAPE"), (torch.zeros(128, dtype=torch.float64)[::2], "SHAPE"),
+                        (f[:0], "SHAPE"), (torch.zeros(1, dtype=torch.float64).expand(64), "SHAPE")):
+        with pytest.raises(api.MXError) as e:
+            api.Rope(128, bad)
+        assert e.value.status == getattr(api, "MX_ERR_" + status), bad.shape
+    for good in (f, torch.zeros(65, dtype=torch.float64), f.reshape(8, 8), P):   # an address stands for itself
+        api.Rope(128, good)
