@@ -300,7 +300,7 @@ class KVCache:
     """An mxkv_cache over torch tensors, which are kept alive here: k and v are
     [pages][heads][page_size][dim] (MXKV_HEADS_FIRST) or [pages][page_size][heads][dim]
     (MXKV_SLOTS_FIRST), dense within a page; for MX_E4M3 bytes, with the scales ks, vs
-    [pages][..][..][dim / 32]."""
+    [pages][..][..][dim / 32]. Their types are the format's, or whole numbers of its size that stand for the bits."""
 
     def __init__(self, fmt: int, k, v, ks=None, vs=None, order: int = MXKV_HEADS_FIRST):
         pages, a, b, dim = k.shape
@@ -310,8 +310,10 @@ class KVCache:
                 continue
             if tuple(t.shape) != (pages, a, b, d) or not t[0].is_contiguous() or (pages > 1 and t.stride(0) * unit != stride):
                 raise MXError(MX_ERR_SHAPE, "KVCache")
-        if any(t.element_size() != (1 if fmt == MX_E4M3 else 2) for t in (k, v)) or any(t.element_size() != 1 for t in (ks, vs) if t is not None):
-            raise MXError(MX_ERR_FORMAT, "KVCache")
+        plane = {MX_F16: "float16", MX_BF16: "bfloat16", MX_E4M3: "float8_e4m3fn"}.get(fmt)
+        for t, size, kind in ((k, 1 if fmt == MX_E4M3 else 2, plane), (v, 1 if fmt == MX_E4M3 else 2, plane), (ks, 1, "float8_e8m0fnu"), (vs, 1, "float8_e8m0fnu")):
+            if t is not None and (t.element_size() != size or (t.dtype.is_floating_point and str(t.dtype) != f"torch.{kind}")):
+                raise MXError(MX_ERR_FORMAT, "KVCache")
         heads, page_size = (a, b) if order == MXKV_HEADS_FIRST else (b, a)
         self.tensors = (k, v, ks, vs)
         self.c = _Cache(fmt, order, pages, page_size, heads, dim, stride, _ptr(k), _ptr(v), _ptr(ks), _ptr(vs))

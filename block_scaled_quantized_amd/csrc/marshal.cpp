@@ -55,8 +55,13 @@ bool heads(const at::Tensor& t, mx_heads* h) {
   return true;
 }
 
-// Whether the tensor's elements have the size of format f's (a wrong one would be read past its end).
-bool fits(const at::Tensor& t, int f) { return t.element_size() == (f == MX_F32 ? 4 : 2); }
+// Whether the tensor's elements are format f's: of its size (a wrong one would be read past its end), and where they are
+// floating ones, of its type. Whole numbers of that size stand for their bits.
+bool fits(const at::Tensor& t, int f) {
+  const at::ScalarType s = t.scalar_type();
+  if (t.element_size() != (f == MX_F32 ? 4 : 2)) return false;
+  return !at::isFloatingType(s) || s == (f == MX_F32 ? at::kFloat : f == MX_BF16 ? at::kBFloat16 : at::kHalf);
+}
 
 // The address of a dense int32 tensor of this shape; None: NULL.
 bool ints(PyObject* o, at::IntArrayRef shape, const int32_t** p) {

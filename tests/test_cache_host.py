@@ -420,3 +420,41 @@ def test_rope_refuses_frequencies_that_are_not_rot_dim_halves_of_doubles():
         assert e.value.status == getattr(api, "MX_ERR_" + status), bad.shape
     for good in (f, torch.zeros(65, dtype=torch.float64), f.reshape(8, 8), P):   # an address stands for itself
         api.Rope(128, good)
+
+
+def test_python_refuses_tensors_of_another_floating_type():
+    """binary16 given as MX_BF16 has the right size and the wrong values; whole-number tensors stand for their bits."""
+    import torch
+
+    def x(kind, *shape):
+        return torch.zeros(*shape, dtype=kind)
+
+    def ints(*shape):
+        return torch.zeros(*shape, dtype=torch.int32)
+
+    half, bf16 = torch.float16, torch.bfloat16
+    rope = api.Rope(64, P)
+    for f, kind, other in ((api.MX_F16, half, bf16), (api.MX_BF16, bf16, half)):
+        for a, b in ((other, kind), (kind, other)):
+            with pytest.raises(api.MXError) as e:
+                api.mxrope_run(f, rope, x(a, 4, 8, 64), x(b, 4, 8, 64), ints(4), stream=0)
+            assert e.value.status == api.MX_ERR_FORMAT
+    k = x(half, 5, 2, 16, 64)
+    c = api.KVCache(api.MX_F16, k, k)
+    for bad in (dict(k=x(bf16, 4, 2, 64)), dict(v=x(bf16, 4, 2, 64)), dict(q=x(bf16, 4, 8, 64)), dict(q_out=x(bf16, 4, 8, 64))):
+        kw = dict(dict(k=x(half, 4, 2, 64), v=x(half, 4, 2, 64), q=x(half, 4, 8, 64), q_out=x(half, 4, 8, 64)), **bad)
+        with pytest.raises(api.MXError) as e:
+            api.mxkv_append_run(c, api.MX_F16, kw["k"], kw["v"], ints(4), ints(3, 5), rope=rope, q=kw["q"], q_out=kw["q_out"], stream=0)
+        assert e.value.status == api.MX_ERR_FORMAT, bad
+    for q, out in ((bf16, half), (half, bf16)):
+        with pytest.raises(api.MXError) as e:
+            api.mxattn_decode_run(c, api.MX_F16, x(q, 3, 8, 64), x(out, 3, 8, 64), ints(3, 5), ints(3), 80, 0.1, stream=0)
+        assert e.value.status == api.MX_ERR_FORMAT
+    codes, scales = x(torch.uint8, 5, 2, 16, 64), x(torch.uint8, 5, 2, 16, 2)
+    for args in ((api.MX_BF16, k, k), (api.MX_F16, k, k.bfloat16()), (api.MX_E4M3, codes.view(torch.float8_e5m2), codes, scales, scales),
+                 (api.MX_E4M3, codes, codes, scales, scales.view(torch.float8_e4m3fn))):
+        with pytest.raises(api.MXError) as e:
+            api.KVCache(*args)
+        assert e.value.status == api.MX_ERR_FORMAT
+    api.KVCache(api.MX_E4M3, codes.view(torch.float8_e4m3fn), codes, scales.view(torch.float8_e8m0fnu), scales)
+    api.KVCache(api.MX_BF16, k.view(torch.int16), k.view(torch.int16))
