@@ -255,10 +255,17 @@ def int_shapes(fw: int, K: int, N: int):
 
 # ---- the decode step's cache: rotary positions, append, attention, pages ------------------------
 
+def _ints(where: str, *values) -> None:
+    """Refuses numbers that ctypes would cut to their low 32 bits."""
+    if not all(-1 << 31 <= v < 1 << 31 for v in values):
+        raise MXError(MX_ERR_SHAPE, where)
+
+
 class Rope:
     """An mxrope: freq is a device tensor of rot_dim / 2 doubles (or more), which is kept alive here, or an address."""
 
     def __init__(self, rot_dim: int, freq, layout: int = MXROPE_HALF, factor: float = 1.0):
+        _ints("Rope", rot_dim)
         if hasattr(freq, "data_ptr"):
             if not freq.dtype.is_floating_point or freq.element_size() != 8:
                 raise MXError(MX_ERR_FORMAT, "Rope")
@@ -271,6 +278,7 @@ class Rope:
 
 def mxrope_freqs_host(rot_dim: int, base: float, rule: int = MXROPE_PLAIN, params=()):
     """(list of rot_dim / 2 angles per position, factor of cos and sin) of a frequency rule."""
+    _ints("mxrope_freqs_host", rot_dim, rule)
     freq, factor = (ctypes.c_double * max(1, rot_dim // 2))(), ctypes.c_float()
     par = (ctypes.c_double * 4)(*params) if len(params) else None
     _check(_lib.mxrope_freqs_host(rot_dim, base, rule, par, freq, ctypes.addressof(factor)), "mxrope_freqs_host")
@@ -338,6 +346,7 @@ def mxkv_append_run(cache: KVCache, f: int, k, v, positions, table, seq=None, ro
 
 
 def mxattn_decode_workspace_size(cache: KVCache, seqs: int, q_heads: int, max_len: int, window: int = 0) -> int:
+    _ints("mxattn_decode_workspace_size", seqs, q_heads, max_len, window)
     return int(_lib.mxattn_decode_workspace_size(cache.ref, seqs, q_heads, max_len, window))
 
 
@@ -365,6 +374,7 @@ class KVPool:
     def __init__(self, pages: int, page_size: int, seqs: int, cols: int):
         h = _vp()
         self.handle = None
+        _ints("mxkv_pool_create", pages, page_size, seqs, cols)
         _check(_lib.mxkv_pool_create(ctypes.byref(h), pages, page_size, seqs, cols), "mxkv_pool_create")
         self.handle, self.pages, self.seqs, self.cols = h.value, pages, seqs, cols
 
@@ -380,20 +390,24 @@ class KVPool:
             pass
 
     def resize(self, seq: int, tokens: int):
+        _ints("mxkv_pool_resize", seq, tokens)
         pair, n = (ctypes.c_int32 * 2)(), _i()
         _check(_lib.mxkv_pool_resize(self.handle, seq, tokens, pair, ctypes.byref(n)), "mxkv_pool_resize")
         return [(pair[0], pair[1])] if n.value else []
 
     def fork(self, src: int, dst: int) -> None:
+        _ints("mxkv_pool_fork", src, dst)
         _check(_lib.mxkv_pool_fork(self.handle, src, dst), "mxkv_pool_fork")
 
     def reorder(self, source) -> None:
         if len(source) != self.seqs:
             raise MXError(MX_ERR_SHAPE, "mxkv_pool_reorder")
+        _ints("mxkv_pool_reorder", *source)
         _check(_lib.mxkv_pool_reorder(self.handle, (ctypes.c_int32 * self.seqs)(*source)), "mxkv_pool_reorder")
 
     def compact(self, max_pairs: int | None = None):
         most = self.pages if max_pairs is None else max_pairs
+        _ints("mxkv_pool_compact", most)
         pairs, n = (ctypes.c_int32 * max(1, 2 * most))(), _i()
         _check(_lib.mxkv_pool_compact(self.handle, pairs, most, ctypes.byref(n)), "mxkv_pool_compact")
         return [(pairs[2 * i], pairs[2 * i + 1]) for i in range(n.value)]

@@ -19,6 +19,10 @@ struct TypeError : std::exception {
   const char* what() const noexcept override { return "a torch tensor was expected"; }
 };
 struct PythonError : std::exception {};  // already set
+struct Refused : std::exception {  // with a status of the library
+  int status;
+  explicit Refused(int s) : status(s) {}
+};
 
 const at::Tensor& tensor(PyObject* o) {
   if (!THPVariable_Check(o)) throw TypeError();
@@ -31,8 +35,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
-int narrow(PyObject* o) {  // to int, as ctypes converts: the low 32 bits
-  return (int)integer(o);
+int narrow(PyObject* o, int status) {  // a number that is no int is refused with this status
+  int past = 0;
+  const int64_t v = PyLong_AsLongLongAndOverflow(o, &past);
+  if (v == -1 && !past && PyErr_Occurred()) throw PythonError();
+  if (past || v < INT_MIN || v > INT_MAX) throw Refused(status);
+  return (int)v;
 }
 
 double number(PyObject* o) {
@@ -114,7 +122,7 @@ int rope(PyObject* const* a) {
   mx_heads hx, ho;
   const int32_t* positions;
   if (!heads(x, &hx) || !heads(out, &ho) || x.sizes() != out.sizes() || !ints(a[4], x.sizes().slice(0, 1), &positions)) return MX_ERR_SHAPE;
-  const int f = narrow(a[0]), tokens = (int)x.size(0), dim = (int)x.size(2), inverse = narrow(a[5]);
+  const int f = narrow(a[0], MX_ERR_FORMAT), tokens = (int)x.size(0), dim = (int)x.size(2), inverse = integer(a[5]) != 0;
   if (!fits(x, f) || !fits(out, f)) return MX_ERR_FORMAT;
   const mxrope* r = address<mxrope>(a[1]);
   void* stream = stream_of(a[6]);
@@ -126,7 +134,7 @@ int append(PyObject* const* a) {
   const mxkv_cache* cache = address<mxkv_cache>(a[0]);
   mx_heads h[4];
   bool given[4];
-  const int f = narrow(a[1]);
+  const int f = narrow(a[1], MX_ERR_FORMAT);
   const int64_t n = tensor(a[2]).dim() == 3 ? tensor(a[2]).size(0) : -1;
   const int place[4] = {2, 3, 8, 9};
   for (int i = 0; i < 4; i++) {
@@ -166,14 +174,19 @@ int attention(PyObject* const* a) {
   size_t bytes = 0;
   if (THPVariable_Check(a[12])) {
     const at::Tensor& t = tensor(a[12]);
+    if (!t.is_contiguous()) return MX_ERR_SHAPE;
     workspace = t.data_ptr(), bytes = t.nbytes();
   } else {
     workspace = address<void>(a[12]);
   }
-  if (a[13] != Py_None) bytes = (size_t)integer(a[13]);
-  const int f = narrow(a[1]), max_len = narrow(a[6]);
+  if (a[13] != Py_None) {
+    const int64_t given = integer(a[13]);
+    if (given < 0 || (THPVariable_Check(a[12]) && (size_t)given > bytes)) return MX_ERR_SHAPE;
+    bytes = (size_t)given;
+  }
+  const int f = narrow(a[1], MX_ERR_FORMAT), max_len = narrow(a[6], MX_ERR_SHAPE);
   if (!fits(q, f) || !fits(out, f)) return MX_ERR_FORMAT;
-  const mxattn_opts opts = {(float)number(a[7]), (float)number(a[11]), narrow(a[10])};
+  const mxattn_opts opts = {(float)number(a[7]), (float)number(a[11]), narrow(a[10], MX_ERR_SHAPE)};
   void* stream = stream_of(a[14]);
   return unlocked([&] {
     return mxattn_decode_run(cache, f, &hq, &ho, lse, &table, lengths, starts, max_len, &opts, workspace, bytes, stream);
@@ -186,7 +199,7 @@ int copy(PyObject* const* a) {
   const at::Tensor& t = tensor(a[2]);
   const int32_t* pairs;
   if (t.dim() != 2 || !is_int(t.size(0)) || !ints(a[2], {t.size(0), 2}, &pairs)) return MX_ERR_SHAPE;
-  const int n_layers = narrow(a[1]), n = (int)t.size(0);
+  const int n_layers = narrow(a[1], MX_ERR_SHAPE), n = (int)t.size(0);
   void* stream = stream_of(a[3]);
   return unlocked([&] { return mxkv_copy_run(layers, n_layers, pairs, n, stream); });
 }
@@ -201,6 +214,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t count) {
     return PyLong_FromLong(F(args));
   } catch (const TypeError& e) {
     PyErr_SetString(PyExc_TypeError, e.what());
+  } catch (const Refused& e) {
+    return PyLong_FromLong(e.status);
   } catch (const PythonError&) {
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());

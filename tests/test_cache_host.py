@@ -458,3 +458,31 @@ def test_python_refuses_tensors_of_another_floating_type():
         assert e.value.status == api.MX_ERR_FORMAT
     api.KVCache(api.MX_E4M3, codes.view(torch.float8_e4m3fn), codes, scales.view(torch.float8_e8m0fnu), scales)
     api.KVCache(api.MX_BF16, k.view(torch.int16), k.view(torch.int16))
+
+
+def test_python_refuses_numbers_past_32_bits():
+    """Not cut to their low 32 bits: a window of 2^32 is not none, a length of 2^32 + 5 not five."""
+    import torch
+    q, big = torch.zeros(3, 8, 64, dtype=torch.float16), 1 << 32
+    k, n = torch.zeros(5, 2, 16, 64, dtype=torch.float16), torch.zeros(3, dtype=torch.int32)
+    c, table, ws = api.KVCache(api.MX_F16, k, k), torch.zeros(3, 5, dtype=torch.int32), torch.zeros(64, dtype=torch.uint8)
+
+    def attend(f=api.MX_F16, max_len=80, **kw):
+        return lambda: api.mxattn_decode_run(c, f, q, q, table, n, max_len, 0.1, stream=0, **kw)
+
+    pool = api.KVPool(8, 16, 2, 4)
+    pool.resize(0, 5)
+    bad = [(attend(f=big + api.MX_F16), "FORMAT"), (attend(max_len=big + 80), "SHAPE"), (attend(max_len=-big + 80), "SHAPE"), (attend(window=big), "SHAPE"),
+           (attend(window=big + 7), "SHAPE"), (attend(window=1 << 70), "SHAPE"), (attend(workspace=ws, workspace_bytes=-1), "SHAPE"),
+           (attend(workspace=ws, workspace_bytes=65), "SHAPE"), (attend(workspace=ws[::2]), "SHAPE"), (attend(workspace=ws[:1].expand(64)), "SHAPE"),
+           (lambda: api.mxrope_run(big + api.MX_F16, api.Rope(64, P), q, q, n, stream=0), "FORMAT"),
+           (lambda: api.mxkv_append_run(c, big + api.MX_F16, q[:, :2], q[:, :2], n, table, stream=0), "FORMAT"),
+           (lambda: api.Rope(big + 64, P), "SHAPE"), (lambda: api.mxrope_freqs_host(big + 64, 1e4), "SHAPE"),
+           (lambda: api.mxattn_decode_workspace_size(c, 3, 8, big + 80), "SHAPE"), (lambda: api.KVPool(8, big + 16, 2, 4), "SHAPE"),
+           (lambda: pool.resize(0, big + 7), "SHAPE"), (lambda: pool.resize(big, 7), "SHAPE"), (lambda: pool.fork(0, big + 1), "SHAPE"),
+           (lambda: pool.reorder([0, big]), "SHAPE"), (lambda: pool.compact(big + 1), "SHAPE")]
+    for i, (call, status) in enumerate(bad):
+        with pytest.raises(api.MXError) as e:
+            call()
+        assert e.value.status == getattr(api, "MX_ERR_" + status), i
+    assert pool.lengths().tolist() == [5, 0]
