@@ -261,6 +261,11 @@ def _ints(where: str, *values) -> None:
         raise MXError(MX_ERR_SHAPE, where)
 
 
+def _on_host(*tensors) -> bool:
+    """Whether one of these is a tensor or array in host memory that the GPU cannot read."""
+    return any(t is not None and not isinstance(t, int) and not (hasattr(t, "data_ptr") and (t.is_cuda or t.numel() == 0 or t.is_pinned())) for t in tensors)
+
+
 class Rope:
     """An mxrope: freq is a device tensor of rot_dim / 2 doubles (or more), which is kept alive here, or an address."""
 
@@ -271,7 +276,7 @@ class Rope:
                 raise MXError(MX_ERR_FORMAT, "Rope")
             if not freq.is_contiguous() or freq.numel() < rot_dim // 2:
                 raise MXError(MX_ERR_SHAPE, "Rope")
-        self.freq = freq
+        self.freq, self.host = freq, _on_host(freq)
         self.c = _Rope(rot_dim, layout, _ptr(freq), factor)
         self.ref = ctypes.addressof(self.c)
 
@@ -299,7 +304,7 @@ def _load():
 
 def mxrope_run(f: int, rope: Rope, x, out, positions, inverse: bool = False, stream=None) -> None:
     """x, out: [tokens][heads][dim] (out may be x); positions: int32 [tokens]."""
-    s = (_marshal or _load()).rope(f, rope.ref, x, out, positions, inverse, None if stream is None else _stream(stream))
+    s = (_marshal or _load()).rope(f, rope.ref, x, out, positions, inverse, None if stream is None else _stream(stream), rope.host)
     if s:
         raise MXError(s, "mxrope_run")
 
@@ -323,7 +328,7 @@ class KVCache:
             if t is not None and (t.element_size() != size or (t.dtype.is_floating_point and str(t.dtype) != f"torch.{kind}")):
                 raise MXError(MX_ERR_FORMAT, "KVCache")
         heads, page_size = (a, b) if order == MXKV_HEADS_FIRST else (b, a)
-        self.tensors = (k, v, ks, vs)
+        self.tensors, self.host = (k, v, ks, vs), _on_host(k, v, ks, vs)
         self.c = _Cache(fmt, order, pages, page_size, heads, dim, stride, _ptr(k), _ptr(v), _ptr(ks), _ptr(vs))
         self.ref = ctypes.addressof(self.c)
 
@@ -331,7 +336,7 @@ class KVCache:
 def kv_layers(caches):
     """The layers' caches as the array that mxkv_copy_run takes, for callers that keep it."""
     arr = (_Cache * max(1, len(caches)))(*(x.c for x in caches))
-    arr.count, arr.caches = len(caches), list(caches)
+    arr.count, arr.caches, arr.host = len(caches), list(caches), any(x.host for x in caches)
     return arr
 
 
@@ -340,7 +345,7 @@ def mxkv_append_run(cache: KVCache, f: int, k, v, positions, table, seq=None, ro
     """k, v: [tokens][heads][dim]; positions, seq: int32 [tokens]; table: int32 [seqs][cols]; q, q_out:
     [tokens][q heads][dim], turned in the same launch."""
     s = (_marshal or _load()).append(cache.ref, f, k, v, positions, table, seq, rope.ref if rope else None, q, q_out,
-                                     None if stream is None else _stream(stream))
+                                     None if stream is None else _stream(stream), cache.host or (rope is not None and rope.host))
     if s:
         raise MXError(s, "mxkv_append_run")
 
@@ -355,7 +360,7 @@ def mxattn_decode_run(cache: KVCache, f: int, q, out, table, lengths, max_len: i
     """q, out: [seqs][q heads][dim]; table: int32 [seqs][cols]; lengths, starts: int32 [seqs]; lse: fp32
     [seqs][q heads]; workspace: a zero-filled device buffer (a tensor's own size when workspace_bytes is omitted)."""
     s = (_marshal or _load()).attention(cache.ref, f, q, out, table, lengths, max_len, scale, lse, starts, window, softcap,
-                                        workspace, workspace_bytes, None if stream is None else _stream(stream))
+                                        workspace, workspace_bytes, None if stream is None else _stream(stream), cache.host)
     if s:
         raise MXError(s, "mxattn_decode_run")
 
@@ -363,7 +368,7 @@ def mxattn_decode_run(cache: KVCache, f: int, q, out, table, lengths, max_len: i
 def mxkv_copy_run(caches, pairs, stream=None) -> None:
     """caches: a list of KVCache, or kv_layers of it; pairs: int32 [n][2] of (source, destination) pages."""
     arr = caches if isinstance(caches, ctypes.Array) else kv_layers(caches)
-    s = (_marshal or _load()).copy(ctypes.addressof(arr), arr.count, pairs, None if stream is None else _stream(stream))
+    s = (_marshal or _load()).copy(ctypes.addressof(arr), arr.count, pairs, None if stream is None else _stream(stream), arr.host)
     if s:
         raise MXError(s, "mxkv_copy_run")
 

@@ -10,13 +10,16 @@
 
 #include <climits>
 #include <exception>
+#include <initializer_list>
 
 #include "mxgemm.h"
 
 namespace {
 
 struct TypeError : std::exception {
-  const char* what() const noexcept override { return "a torch tensor was expected"; }
+  const char* text;
+  explicit TypeError(const char* t) : text(t) {}
+  const char* what() const noexcept override { return text; }
 };
 struct PythonError : std::exception {};  // already set
 struct Refused : std::exception {  // with a status of the library
@@ -25,7 +28,7 @@ struct Refused : std::exception {  // with a status of the library
 };
 
 const at::Tensor& tensor(PyObject* o) {
-  if (!THPVariable_Check(o)) throw TypeError();
+  if (!THPVariable_Check(o)) throw TypeError("a torch tensor was expected");
   return THPVariable_Unpack(o);
 }
 
@@ -88,6 +91,18 @@ bool table_of(PyObject* o, mxkv_table* table) {
   return true;
 }
 
+// The last check before a call: every tensor that a kernel will read is one that the GPU can (None and addresses pass). `host`: whether
+// one of a descriptor that the caller keeps is not.
+void on_gpu(PyObject* host, std::initializer_list<PyObject*> tensors) {
+  bool ok = host != Py_True;
+  for (PyObject* o : tensors) {
+    if (!THPVariable_Check(o)) continue;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    ok = ok && (t.is_cuda() || t.numel() == 0 || t.is_pinned());
+  }
+  if (!ok) throw TypeError("a tensor on the GPU was expected");
+}
+
 void* stream_of(PyObject* o) {  // None: torch's current stream
   if (o != Py_None) return address<void>(o);
   static PyObject* current = nullptr;  // torch's own function of a device's current stream, kept for good
@@ -116,7 +131,7 @@ int unlocked(F call) {
   return status;
 }
 
-// (f, rope, x, out, positions, inverse, stream)
+// (f, rope, x, out, positions, inverse, stream, host)
 int rope(PyObject* const* a) {
   const at::Tensor &x = tensor(a[2]), &out = tensor(a[3]);
   mx_heads hx, ho;
@@ -125,11 +140,12 @@ int rope(PyObject* const* a) {
   const int f = narrow(a[0], MX_ERR_FORMAT), tokens = (int)x.size(0), dim = (int)x.size(2), inverse = integer(a[5]) != 0;
   if (!fits(x, f) || !fits(out, f)) return MX_ERR_FORMAT;
   const mxrope* r = address<mxrope>(a[1]);
+  on_gpu(a[7], {a[2], a[3], a[4]});
   void* stream = stream_of(a[6]);
   return unlocked([&] { return mxrope_run(f, r, tokens, dim, &hx, &ho, positions, inverse, stream); });
 }
 
-// (cache, f, k, v, positions, table, seq, rope, q, q_out, stream)
+// (cache, f, k, v, positions, table, seq, rope, q, q_out, stream, host)
 int append(PyObject* const* a) {
   const mxkv_cache* cache = address<mxkv_cache>(a[0]);
   mx_heads h[4];
@@ -148,13 +164,15 @@ int append(PyObject* const* a) {
   mxkv_table table;
   if (!table_of(a[5], &table) || !ints(a[4], {n}, &positions) || !ints(a[6], {n}, &seq)) return MX_ERR_SHAPE;
   const mxrope* r = address<mxrope>(a[7]);
+  on_gpu(a[11], {a[2], a[3], a[4], a[5], a[6], a[8], a[9]});
   void* stream = stream_of(a[10]);
   return unlocked([&] {
     return mxkv_append_run(cache, f, (int)n, &h[0], &h[1], positions, seq, &table, r, given[2] ? &h[2] : nullptr, given[3] ? &h[3] : nullptr, stream);
   });
 }
 
-// (cache, f, q, out, table, lengths, max_len, scale, lse, starts, window, softcap, workspace, workspace_bytes, stream)
+// (cache, f, q, out, table, lengths, max_len, scale, lse, starts, window, softcap, workspace, workspace_bytes, stream,
+//  host)
 int attention(PyObject* const* a) {
   const mxkv_cache* cache = address<mxkv_cache>(a[0]);
   const at::Tensor &q = tensor(a[2]), &out = tensor(a[3]);
@@ -187,19 +205,21 @@ int attention(PyObject* const* a) {
   const int f = narrow(a[1], MX_ERR_FORMAT), max_len = narrow(a[6], MX_ERR_SHAPE);
   if (!fits(q, f) || !fits(out, f)) return MX_ERR_FORMAT;
   const mxattn_opts opts = {(float)number(a[7]), (float)number(a[11]), narrow(a[10], MX_ERR_SHAPE)};
+  on_gpu(a[15], {a[2], a[3], a[4], a[5], a[8], a[9], a[12]});
   void* stream = stream_of(a[14]);
   return unlocked([&] {
     return mxattn_decode_run(cache, f, &hq, &ho, lse, &table, lengths, starts, max_len, &opts, workspace, bytes, stream);
   });
 }
 
-// (layers, n_layers, pairs, stream)
+// (layers, n_layers, pairs, stream, host)
 int copy(PyObject* const* a) {
   const mxkv_cache* layers = address<mxkv_cache>(a[0]);
   const at::Tensor& t = tensor(a[2]);
   const int32_t* pairs;
   if (t.dim() != 2 || !is_int(t.size(0)) || !ints(a[2], {t.size(0), 2}, &pairs)) return MX_ERR_SHAPE;
   const int n_layers = narrow(a[1], MX_ERR_SHAPE), n = (int)t.size(0);
+  on_gpu(a[4], {a[2]});
   void* stream = stream_of(a[3]);
   return unlocked([&] { return mxkv_copy_run(layers, n_layers, pairs, n, stream); });
 }
@@ -228,7 +248,7 @@ constexpr PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<F, COUNT>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<rope, 7>("rope"), method<append, 11>("append"), method<attention, 15>("attention"), method<copy, 4>("copy"),
+PyMethodDef methods[] = {method<rope, 8>("rope"), method<append, 12>("append"), method<attention, 16>("attention"), method<copy, 5>("copy"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

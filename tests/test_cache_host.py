@@ -486,3 +486,26 @@ def test_python_refuses_numbers_past_32_bits():
             call()
         assert e.value.status == getattr(api, "MX_ERR_" + status), i
     assert pool.lengths().tolist() == [5, 0]
+
+
+def test_python_refuses_host_tensors():
+    """A host tensor's address means nothing to a kernel, which would fault on it: a TypeError once all else is in order."""
+    import torch
+
+    def half(*shape):
+        return torch.zeros(*shape, dtype=torch.float16)
+
+    def ints(*shape):
+        return torch.zeros(*shape, dtype=torch.int32)
+
+    k = half(5, 2, 16, 64)
+    c = api.KVCache(api.MX_F16, k, k)
+    freq = torch.zeros(32, dtype=torch.float64)
+    for call in (lambda: api.mxrope_run(api.MX_F16, api.Rope(64, P), half(4, 8, 64), half(4, 8, 64), ints(4), stream=0),
+                 lambda: api.mxrope_run(api.MX_F16, api.Rope(64, freq), half(4, 8, 64), half(4, 8, 64), ints(4), stream=0),
+                 lambda: api.mxkv_append_run(c, api.MX_F16, half(4, 2, 64), half(4, 2, 64), ints(4), ints(4, 5), stream=0),
+                 lambda: api.mxattn_decode_run(c, api.MX_F16, half(3, 8, 64), half(3, 8, 64), ints(3, 5), ints(3), 80, 0.1, stream=0),
+                 lambda: api.mxkv_copy_run([c], ints(4, 2), stream=0), lambda: api.mxkv_copy_run(api.kv_layers([c]), ints(4, 2), stream=0)):
+        with pytest.raises(TypeError, match="GPU"):
+            call()
+    api.mxkv_copy_run([], ints(0, 2), stream=0)                     # nothing is read
