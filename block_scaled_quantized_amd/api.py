@@ -297,7 +297,10 @@ def _load():
     """The module that turns tensors into descriptors for the calls below (csrc/marshal.cpp); it needs torch."""
     global _marshal
     import torch  # noqa: F401  (loads the libraries that the module is linked to)
-    from . import _marshal as m
+    try:
+        from . import _marshal as m
+    except ImportError as e:
+        raise ImportError(f"the module _marshal.so is missing or does not load: build it with `python -m block_scaled_quantized_amd.build`, with torch installed ({e})") from e
     _marshal = m
     return m
 

@@ -3,7 +3,7 @@
 Every source is compiled for gfx950 only, with packed-fp32 instructions disabled
 (``-Xclang -target-feature -Xclang -packed-fp32-ops``). Objects go to ``_build/``; the shared
 library lands next to this file, and beside it the Python binding's marshalling module (host code, against
-torch's headers). ``python -m block_scaled_quantized_amd.build`` runs it.
+torch's headers; left out where torch is not installed). ``python -m block_scaled_quantized_amd.build`` runs it.
 """
 from __future__ import annotations
 
@@ -45,11 +45,21 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _marshal() -> str:
-    """Compile csrc/marshal.cpp (torch's Tensor accessors, no GPU code)."""
+def _marshal() -> str | None:
+    """Compile csrc/marshal.cpp (torch's Tensor accessors, no GPU code). None, and a message, where torch, its headers,
+    Python's or a host compiler are missing: the library itself needs none of them."""
+    import shutil
     import sysconfig
-    import torch
-    home = os.path.dirname(torch.__file__)
+    try:
+        import torch
+        home = os.path.dirname(torch.__file__)
+        need = [os.path.join(home, "include", "ATen", "core", "Tensor.h"), os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+        missing = [p for p in need if not os.path.exists(p)] + ([] if shutil.which("g++") else ["g++"])
+    except ImportError:
+        missing = ["torch"]
+    if missing:
+        print(f"_marshal.so is not built: no {', '.join(missing)} here (the Python binding's cache calls need it; the library does not)")
+        return None
     obj = os.path.join(BUILD, "marshal.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f"-I{INCLUDE}", f"-isystem{home}/include", f"-isystem{home}/include/torch/csrc/api/include",
@@ -60,8 +70,13 @@ def _marshal() -> str:
     return obj
 
 
-def _link_marshal(obj: str) -> None:
-    """The module finds libmxgemm.so beside itself; torch's libraries are those the process has loaded."""
+def _link_marshal(obj: str | None) -> None:
+    """The module finds libmxgemm.so beside itself; torch's libraries are those the process has loaded. One of an earlier
+    build goes where there is no new one."""
+    if obj is None:
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        return
     import torch
     tmp = MARSHAL + ".tmp"
     cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, f"-L{HERE}", "-lmxgemm", "-Wl,-rpath,$ORIGIN",
