@@ -481,7 +481,7 @@ extern "C" int mxrope_freqs_host(int rot_dim, double base, int rule, const doubl
     }
     freq[i] = k == 1 ? f : (1 - k) * f / params[0] + k * f;
   }
-  *factor = rule == MXROPE_YARN ? (float)(0.1 * std::log(params[0]) + 1.0) : 1.0f;
+  *factor = rule == MXROPE_YARN && params[0] > 1 ? (float)(0.1 * std::log(params[0]) + 1.0) : 1.0f;
   return MX_OK;
 }
 

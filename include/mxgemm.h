@@ -320,7 +320,7 @@ typedef struct {
  *                 k = clamp((t_i - low) / (high - low), 0, 1): (1 - k) f_i / s + k f_i;
  *  MXROPE_YARN    params {s, L, fast, slow}: r_i = clamp((i - a) / max(c - a, 0.001), 0, 1) with a and c
  *                 the pair indexes that make `fast` and `slow` turns over L, rounded down and up and
- *                 cut to 0 and rot_dim - 1: r f_i / s + (1 - r) f_i, and factor 0.1 ln(s) + 1. */
+ *                 cut to 0 and rot_dim - 1: r f_i / s + (1 - r) f_i, and factor 0.1 ln(s) + 1 (1 for s <= 1). */
 typedef enum { MXROPE_PLAIN = 0, MXROPE_LINEAR = 1, MXROPE_NTK = 2, MXROPE_BANDS = 3, MXROPE_YARN = 4 } mxrope_rule;
 
 /* mxrope_freqs_host -- freq[rot_dim/2] (host memory) and *factor of a frequency rule. params: the

@@ -509,3 +509,11 @@ def test_python_refuses_host_tensors():
         with pytest.raises(TypeError, match="GPU"):
             call()
     api.mxkv_copy_run([], ints(0, 2), stream=0)                     # nothing is read
+
+
+@pytest.mark.parametrize("s", [1e-6, 0.25, 0.999, 1.0, 1.5, 16.0])
+def test_yarn_factor_is_1_where_nothing_is_stretched(s):
+    """The factor makes up for a stretched context: 0.1 ln s + 1 above s = 1, 1 up to it (below 1 otherwise, and negative under
+    s = e^-10)."""
+    _, factor = api.mxrope_freqs_host(64, 1e4, api.MXROPE_YARN, (s, 4096.0, 32.0, 1.0))
+    assert factor == np.float32(0.1 * math.log(s) + 1 if s > 1 else 1.0)
