@@ -502,9 +502,11 @@ extern "C" int mxrope_run(int f, const mxrope* rope, int tokens, int dim, const 
   RopeArgs a = rope_args(rope, tokens, dim, x, out, positions, inverse, 16 / bytes, layout);
   a.stream = 2ll * tokens * x->heads * dim * bytes >= kStreamBytes;
   tile(a, layout == kOddHalves ? kStageBytes / (dim * bytes) : 1 << 20);
+  // at most tokens + 1024, but a workgroup per kStageBytes of staged rows
+  if (blocks_of(a) >= 1 << 24) return MX_ERR_SHAPE;
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
-  const dim3 grid((unsigned)blocks_of(a));  // at most tokens + 1024
+  const dim3 grid((unsigned)blocks_of(a));
   if (f == MX_F16) rope_launch<_Float16>(a, layout, grid, st);
   else if (f == MX_BF16) rope_launch<__bf16>(a, layout, grid, st);
   else rope_launch<float>(a, layout, grid, st);

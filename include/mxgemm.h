@@ -336,7 +336,8 @@ int mxrope_freqs_host(int rot_dim, double base, int rule, const double* params, 
  * applied to the output's gradient. f: MX_F16, MX_BF16 or MX_F32 (x and out). Angles are reduced
  * in 64 bits (far positions keep their phase), the products are formed in fp32 and rounded once.
  * x->heads == out->heads; 8 <= dim <= 256, dim % 8 == 0; 0 <= tokens <= MX_MAX_DIM (0: nothing is
- * done), 1 <= heads <= 65536; positions: int32 [tokens], of any sign. out may be x itself (same data and strides);
+ * done), 1 <= heads <= 65536, and fewer than 2^24 workgroups (MX_ERR_SHAPE; only where rot_dim / 2 is not a multiple
+ * of 16 bytes of elements and x has more than 200 GB); positions: int32 [tokens], of any sign. out may be x itself (same data and strides);
  * otherwise the two must not overlap, and no two rows of out may.
  */
 int mxrope_run(int f, const mxrope* rope, int tokens, int dim, const mx_heads* x, const mx_heads* out,

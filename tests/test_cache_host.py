@@ -517,3 +517,12 @@ def test_yarn_factor_is_1_where_nothing_is_stretched(s):
     s = e^-10)."""
     _, factor = api.mxrope_freqs_host(64, 1e4, api.MXROPE_YARN, (s, 4096.0, 32.0, 1.0))
     assert factor == np.float32(0.1 * math.log(s) + 1 if s > 1 else 1.0)
+
+
+def test_rope_refuses_more_workgroups_than_a_launch_has():
+    """Halves that begin within a unit take a workgroup for every 16 KB of rows: 2^20 tokens of 65536 heads of 256 fp32 would be 2^32
+    of them, which a 32-bit grid holds as none."""
+    rows = dict(n=65536, token=65536 * 256, head=256)
+    for tokens, n, status in ((1 << 20, 65536, api.MX_ERR_SHAPE), (1 << 20, 257, api.MX_ERR_SHAPE)):
+        x, out = heads(**dict(rows, n=n)), heads(2 * P, **dict(rows, n=n))
+        assert run_rope(f=api.MX_F32, r=rope(rot=2), tokens=tokens, dim=256, x=x, out=out) == status
