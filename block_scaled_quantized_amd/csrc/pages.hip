@@ -54,16 +54,16 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(Planes planes, Shape dat
   else copy_words(s, scale, pairs, n_pairs, pages, block);
 }
 
-// False where the numbers do not fit the kernel's 32-bit words of a page.
-bool shape_of(int64_t page_bytes, int64_t stride_bytes, int word, int n_pairs, Shape& s, int64_t& blocks) {
+// False where a page has 2^30 words or more (a launch numbers the words of its pairs in 31 bits).
+bool shape_of(int64_t page_bytes, int64_t stride_bytes, int word, Shape& s) {
   if (page_bytes / word >= (int64_t)1 << 30) return false;
   s.words = (int)(page_bytes / word);
   s.stride = stride_bytes / word;
   s.div = FastDiv((uint32_t)s.words);
-  blocks = ceil_div((int64_t)s.words * n_pairs, (int64_t)kThreads);
-  s.blocks = (int)blocks;
-  return blocks < 1 << 23;
+  return true;
 }
+
+int blocks_of(const Shape& s, int n_pairs) { return (int)ceil_div((int64_t)s.words * n_pairs, (int64_t)kThreads); }
 
 }  // namespace
 
@@ -84,13 +84,13 @@ extern "C" int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32
   const int bytes = mx8 ? 1 : 2;
   const int64_t elems = (int64_t)c.heads * c.page_size * c.dim;
   Shape data = {}, scale = {};
-  int64_t blocks = 0, scale_blocks = 0;
-  if (!shape_of(elems * bytes, c.page_stride * bytes, 16, n_pairs, data, blocks)) return MX_ERR_SHAPE;
+  if (!shape_of(elems * bytes, c.page_stride * bytes, 16, data)) return MX_ERR_SHAPE;
   int word = 16;  // a page's scales need not be whole 16-byte words
   if (mx8) {
     while (word > 1 && ((elems / 32) % word || (c.page_stride / 32) % word)) word /= 4;
-    if (!shape_of(elems / 32, c.page_stride / 32, word, n_pairs, scale, scale_blocks)) return MX_ERR_SHAPE;
+    if (!shape_of(elems / 32, c.page_stride / 32, word, scale)) return MX_ERR_SHAPE;  // (fewer words than the data has)
   }
+  const int most = (int)(((int64_t)1 << 31) - kThreads) / data.words;  // pairs of one launch
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
   for (int first = 0; first < n_layers; first += kLayers) {
@@ -100,9 +100,14 @@ extern "C" int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32
       const mxkv_cache& l = layers[first + i];
       p.p[i][0] = (uint8_t*)l.k, p.p[i][1] = (uint8_t*)l.v, p.p[i][2] = (uint8_t*)l.ks, p.p[i][3] = (uint8_t*)l.vs;
     }
-    hipLaunchKernelGGL(copy_kernel, dim3((unsigned)(blocks + scale_blocks), (unsigned)n, 2), dim3(kThreads), 0, st, p, data, scale,
-                       word, pairs, n_pairs, c.pages);
-    if (int s = launch_status()) return s;
+    for (int at = 0; at < n_pairs;) {
+      const int count = n_pairs - at < most ? n_pairs - at : most;
+      data.blocks = blocks_of(data, count), scale.blocks = blocks_of(scale, count);
+      hipLaunchKernelGGL(copy_kernel, dim3((unsigned)(data.blocks + scale.blocks), (unsigned)n, 2), dim3(kThreads), 0, st, p, data, scale,
+                         word, pairs + 2 * (int64_t)at, count, c.pages);
+      if (int s = launch_status()) return s;
+      at += count;
+    }
   }
   return sync_check(MX_OK, st);
 }

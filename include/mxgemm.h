@@ -432,7 +432,7 @@ size_t mxattn_decode_workspace_size(const mxkv_cache* cache, int seqs, int q_hea
  * layer. pairs: int32 [n_pairs][2] on the device. Pairs run in no order: the destinations must be
  * distinct, and none of them a source. Pairs with a page out of range, or of a page with itself, are
  * ignored. layers: host array, read before the call returns. n_layers, n_pairs: 0 .. MX_MAX_DIM (0:
- * nothing is done). MX_ERR_SHAPE also where the layers' geometry differs.
+ * nothing is done). MX_ERR_SHAPE also where the layers' geometry differs, and for pages of 16 GiB of keys and more.
  */
 int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32_t* pairs, int n_pairs, void* stream);
 

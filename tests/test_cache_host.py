@@ -526,3 +526,21 @@ def test_rope_refuses_more_workgroups_than_a_launch_has():
     for tokens, n, status in ((1 << 20, 65536, api.MX_ERR_SHAPE), (1 << 20, 257, api.MX_ERR_SHAPE)):
         x, out = heads(**dict(rows, n=n)), heads(2 * P, **dict(rows, n=n))
         assert run_rope(f=api.MX_F32, r=rope(rot=2), tokens=tokens, dim=256, x=x, out=out) == status
+
+
+def test_copy_takes_every_number_of_pairs():
+    """Up to MX_MAX_DIM pairs, whatever a page's size; a page's plane of 16 GiB and more is refused."""
+    import torch
+
+    def run(c, n):
+        arr = (api._Cache * 1)(c)
+        return lib.mxkv_copy_run(at(arr), 1, P, n, None)
+    if torch.cuda.is_available():
+        pytest.skip("needs a machine without a GPU: valid calls end at the missing device")
+    big = dict(page_size=256, heads=8, dim=128, pages=1 << 16, page_stride=256 * 8 * 128)
+    for kw in (dict(fmt=api.MX_F16), dict(fmt=api.MX_E4M3)):
+        for n in (1, 1 << 15, 1 << 17, 1 << 20):
+            assert run(cache(**big, **kw), n) == api.MX_ERR_ARCH, (kw, n)
+    huge = dict(fmt=api.MX_F16, page_size=1 << 20, heads=32, dim=256, pages=2, page_stride=(1 << 20) * 32 * 256)
+    assert run(cache(**huge), 1) == api.MX_ERR_SHAPE
+    assert run(cache(**dict(huge, heads=31, page_stride=(1 << 20) * 31 * 256)), 7) == api.MX_ERR_ARCH

@@ -84,3 +84,26 @@ def test_pool_moves_keep_every_sequence():
     grow(2, 7)
     check()
     pool.close()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_copy_pairs_of_several_launches(kind):
+    """A list of pairs, most of them ignored, whose words pass 2^31: valid ones at its ends and at the launches' borders."""
+    api = require_gpu()
+    page, heads, dim = 256, 8, 128
+    words = page * heads * dim * (1 if kind == "e4m3" else 2) // 16
+    most = (2 ** 31 - 256) // words
+    n = 2 * most + 5
+    say(f"copy {kind}: {n} pairs of {words} words")
+    c = Cache(kind, "heads", 12, page, heads, dim, 3)
+    planes = c.planes + [s for s in c.scales if s is not None]
+    before = [t.cpu().clone() for t in planes]
+    pairs = np.full((n, 2), -1, np.int32)
+    real = {0: (0, 6), most - 1: (1, 7), most: (2, 8), 2 * most - 1: (3, 9), 2 * most: (4, 10), n - 1: (5, 11)}
+    for i, p in real.items():
+        pairs[i] = p
+    api.mxkv_copy_run([c.c], dev(pairs))
+    torch.cuda.synchronize()
+    for got, w in zip(planes, before):
+        w[6:] = w[:6]
+        assert torch.equal(got.cpu().view(torch.uint8), w.view(torch.uint8))
