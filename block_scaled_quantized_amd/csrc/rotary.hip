@@ -6,8 +6,9 @@
 // the tokens' cosines and sines once into LDS, one (token, pair) per thread, while its first rows
 // are on their way, and every head reads them from there. The angle is reduced in 64 bits:
 // pos * f / 2 pi loses about 2^-52 of its value (2^20 positions: 2^-32 turns), where 32 bits would
-// lose the phase of far positions altogether; after the reduction to half a turn an fp32 sine and
-// cosine are exact to 2 ulp.
+// lose the phase of far positions altogether. The reduced angle is rounded to fp32 for the sine and cosine (2 ulp),
+// and its rest, up to 2^-25 half turns, turns them on: alone the rounding would be off by 9e-8, far more than
+// 2 ulp of a small one.
 //
 // Rows move in 16-byte units whatever rot_dim is. Halves of whole units are loaded as pairs of units,
 // neighbouring pairs lie in one; halves that begin within a unit (rot_dim / 2 not a multiple of it) are
@@ -97,9 +98,12 @@ MX_DEV void fill_trig(const Rotation& r, const int32_t* __restrict__ pos, int t0
     const int t = by_half.div(i);
     double w = (double)pos[t0 + t] * r.freq[i - t * r.half] * 0.15915494309189533577;  // in turns
     w -= __builtin_rint(w);
+    w += w;  // in half turns
+    const float near = (float)w, rest = (float)(w - near) * 3.14159265358979323846f;
     float s, c;
-    sincospif((float)(w + w), &s, &c);
-    trig[i] = make_float2(c * r.factor, s * r.factor * r.sign);
+    sincospif(near, &s, &c);
+    const float cos_w = __builtin_fmaf(-rest, s, c), sin_w = __builtin_fmaf(rest, c, s);
+    trig[i] = make_float2(cos_w * r.factor, sin_w * r.factor * r.sign);
   }
 }
 
