@@ -4,7 +4,7 @@
 // wave keeps the running maximum m, sum and output of its keys and rescales them where m grows. The
 // cache is read once and bounds the time (each key-value pair of bytes meets the few query heads that
 // share it), so everything else serves its loads: 16 query heads of one cache head are the columns of a
-// 16x16x32 matrix instruction (columns without a head idle: the matrix cores have more than ten times
+// 16x16x32 matrix instruction (columns without a head idle: the matrix cores have at least eight times
 // the rate that the memory asks of them), K and V go from global memory to registers with no LDS
 // between, up to two tiles ahead, and the keys of long rows are shared evenly among one round of workgroups.
 //
@@ -19,11 +19,13 @@
 // E4M3 elements become 16-bit ones on the way by gfx950's scaled conversion, which takes the block's
 // power of two: a lane's 8 K elements and its V elements of one key lie in one block of 32.
 //
-// Measured (reads of a large array by a row maximum: 6.4 TB/s): 64 x 16384 keys x 8 x 128 E4M3, 2.2 GB, 359 us,
-// 6.2 TB/s; 131072 keys x 8 x 128 fp16, 537 MB, 92 us, 5.8 TB/s; the same bytes over 16 x 8192 keys x 4 x
-// 256, 88 us. Where a call's work is a few grains per workgroup, its time is the chain of dependent memory
+// Measured, us of a call among others on changing inputs (reads of a large array by a row maximum: 6.4 TB/s): 64 x 16384
+// keys x 8 x 128 E4M3, 2.2 GB, 345 us, 6.4 TB/s; 131072 keys x 8 x 128 fp16, 537 MB, 86 us, 6.2 TB/s; the same bytes
+// over 16 x 8192 keys x 4 x 256, 93 us. Where a call's work is a few grains per workgroup, its time is the chain of dependent memory
 // latencies (lengths and pages, keys, and for cut units partials, counter, partials) and the instructions that come from
-// memory: 5.3 us for rows of a few keys, 9.4 us for 8 x 500 keys of 128 (a kernel of one store: 3.6 us).
+// memory: 5.1 us for rows of a few keys, 8.7 to 10.6 us for 8 x 500 keys of 128 (a kernel of one store: 3.6 us).
+// Pairs of times below compare two choices side by side in graphs of calls, as they were when the choice was made: a call
+// takes up to 2 us more there, and boxes differ by a tenth.
 #include <algorithm>
 
 #include "kvcache.h"
@@ -896,7 +898,7 @@ constexpr int kCUs = 256;
 static_assert(2 * kCUs <= kFan * kGroup, "a row's groups are joined in one step");
 // The lengths are known on the device only. The grid is one round of workgroups: one to a CU, whose waves
 // have 128 KB on their way, or two where two tiles per wave are less than that (131072 x 8 x 128 fp16:
-// 92 us with one, 100 with two, which double the partials; 64 x 16384 x 8 x 128 E4M3: 372 and 360); fewer where
+// 92 us with one, 97 with two, which double the partials; 64 x 16384 x 8 x 128 E4M3: 366 and 346); fewer where
 // max_len bounds the grains.
 int workgroups(int D, int fmt, int ht) {
   return kCUs * (tiles_ahead(D, true, ht) * kGrain * 2 * D * (fmt == MX_E4M3 ? 1 : 2) < 131072 ? 2 : 1);
@@ -914,7 +916,8 @@ Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
   const int64_t grains = ceil_div(span, (int64_t)kGrain);
   // Two head tiles, so that the keys of more than 16 query heads are read once, where that is what the time goes
   // to: at 16 grains and more of a workgroup (20 heads of 128 bf16, rows of 8192 keys: 94 -> 57 us at 32 grains; of
-  // 32768: 31.0 and 32.5 at 8; of 4096: 20.5 and 28 at 4). D = 256 has no registers for it.
+  // 32768: 31.0 and 32.5 at 8; of 4096: 20.5 and 28 at 4). Heads above 128 have one tile: a second would take the E4M3 shares' second wave per SIMD
+  // and a merge in two rounds, and is not built.
   const int64_t units = (int64_t)seqs * c->heads * ceil_div(group, 16);
   p.ht = D < 256 && group > 16 && units * grains >= 16 * workgroups(D, c->fmt, 1) ? 2 : 1;
   p.tiles = ceil_div(group, 16 * p.ht);

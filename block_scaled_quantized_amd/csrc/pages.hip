@@ -3,10 +3,10 @@
 // A page's elements lie together in either order, so a copy is a gather of contiguous pieces: the pairs'
 // bytes of a plane are numbered through, each thread takes one 16-byte word and finds its pair by a
 // division by the page's words, exact in one product (a division of 64-bit numbers per workgroup before: 4 pages over 8
-// layers 4.4 -> 3.7 us). Bound by memory: each byte is read and written once (700 pairs of 64 slots x 8 x
-// 128 E4M3 over four layers, 755 MB moved: 136 us, 5.55 TB/s; with two words per thread 145, with four 153
-// before stores were non-temporal). The stores leave the caches to what is read; non-temporal loads gained a
-// little more on large copies but lost a third on pages that the caches still held.
+// layers 4.4 -> 3.7 us in a graph of calls; 4.6 us a call where the host queues each). Bound by memory: each byte is read and written
+// once (700 pairs of 64 slots x 8 x 128 E4M3 over four layers, 755 MB moved: 134 us, 5.6 TB/s, where torch's copy of as
+// much reaches 5.3; with two words per thread 145, with four 153 before stores were non-temporal). The stores leave the caches to what
+// is read; non-temporal loads gained a little more on large copies but lost a third on pages that the caches still held.
 #include "kvcache.h"
 
 using namespace mx;

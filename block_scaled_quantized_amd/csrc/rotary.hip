@@ -12,10 +12,10 @@
 //
 // Rows move in 16-byte units whatever rot_dim is. Halves of whole units are loaded as pairs of units,
 // neighbouring pairs lie in one; halves that begin within a unit (rot_dim / 2 not a multiple of it) are
-// staged in LDS, where each element finds its partner. Measured, 4096 tokens x 32 heads x 128 bf16, 67 MB:
-// 11.9 us with rot_dim = 128 in halves, 12.5 us in pairs, 17 us with rot_dim = 126 in halves (34 us one
-// pair at a time). Append of 8191 tokens, 32 query and 8 cache heads of 128 bf16, 201 MB: 37 us, 5.4 TB/s; into an
-// E4M3 cache 4096 tokens take 19 us.
+// staged in LDS, where each element finds its partner. Measured, us of a call among others on changing inputs, 4096 tokens x
+// 32 heads x 128 bf16, 67 MB: 10.9 with rot_dim = 128 in halves, 11.3 in pairs, 13.9 with rot_dim = 126 in halves (one pair at
+// a time it took twice that). Append of 8191 tokens, 32 query and 8 cache heads of 128 bf16, 201 MB: 35 us, 5.7 TB/s; into an
+// E4M3 cache 4096 tokens take 18 us. Pairs of times below compare two choices side by side in graphs of calls, about 1 us more each.
 #include <cmath>
 #include <type_traits>
 

@@ -441,7 +441,8 @@ int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32_t* pairs, 
  * for the calls above. Host only, queues no GPU work; not safe for concurrent calls on one pool. A new
  * page is always the free one with the lowest number. Sequences may share pages (fork); a page is free
  * when no sequence holds it. Functions that hand out page pairs expect the caller to queue
- * mxkv_copy_run for them before any later write to the cache.
+ * mxkv_copy_run for them before any later write to the cache, and before the pairs of a call that follows a
+ * sequence's shrinking: a page that one call reads can be what a later one writes.
  */
 typedef struct mxkv_pool_state* mxkv_pool;
 
