@@ -84,3 +84,24 @@ def test_infinite_values_stay_infinite(kind, dim, page, n):
         same = np.ones((8, dim), bool)
         same[4:, [3, 5, 8, 9]] = False
         assert np.array_equal(got[same], clean[same])
+
+
+@pytest.mark.parametrize("kind,cache", [("f16", "f16"), ("bf16", "bf16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("page,n", [(16, 200), (24, 200), (16, 2000), (24, 2000)])
+def test_nan_keys_spoil_their_head(kind, cache, page, n):
+    """A NaN in an attended key makes its head's rows and lse NaN, cut to 16 bits or not, and no others."""
+    api = require_gpu()
+    say(f"attention {kind} over {cache}: a NaN key among {n}, pages of {page}")
+    pages = -(-n // page)
+    c = Cache(cache, "heads", pages, page, 2, 64, 21)
+    table = tables([n], page, pages, 3)
+    ws = torch.zeros(max(16, api.mxattn_decode_workspace_size(c.c, 1, 8, n)), dtype=torch.uint8, device="cuda")
+    q = normal((1, 8, 64), kind, 5)
+    for j in (0, n // 2, n - 1):
+        place = (int(table[0, j // page]), 1, j % page, 9)
+        old = c.planes[0][place].clone()
+        c.planes[0][place] = 0x7F if cache == "e4m3" else float("nan")
+        out, lse = torch.zeros_like(q), torch.zeros(1, 8, device="cuda")
+        api.mxattn_decode_run(c.c, fmt_of(api, kind), q, out, dev(table), dev(np.array([n], np.int32)), n, 0.125, lse=lse, workspace=ws)
+        c.planes[0][place] = old
+        assert np.isnan(f64(out)[0, 4:]).all() and np.isnan(f64(lse)[0, 4:]).all() and np.isfinite(f64(out)[0, :4]).all() and np.isfinite(f64(lse)[0, :4]).all(), j
