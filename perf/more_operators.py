@@ -416,12 +416,12 @@ def _own(s):
     api, fmt = h["api"], h["fmt"]
     if c["op"] == "plan":
         if not c["back"]:
-            api.mxkv_plan_run(c["page"], s["table"], s["has"], s["wants"], s["free"], s["n_free"], s["offsets"], *s["maps"], s["status"],
+            api.mxkv_step_run(c["page"], s["table"], s["has"], s["wants"], s["free"], s["n_free"], s["offsets"], *s["maps"], s["status"],
                               lengths_out=s["lengths"], n_free_out=s["left"])
         else:  # taken and given back: the table and the stack end as they began
-            api.mxkv_plan_run(c["page"], s["table"], s["has"], s["wants"], s["free"], s["n_free"], s["offsets"], *s["maps"], s["status"],
+            api.mxkv_step_run(c["page"], s["table"], s["has"], s["wants"], s["free"], s["n_free"], s["offsets"], *s["maps"], s["status"],
                               lengths_out=s["lengths"], n_free_out=s["left"])
-            api.mxkv_plan_run(c["page"], s["table"], s["lengths"], s["has"], s["free"], s["left"], *s["spare"])
+            api.mxkv_step_run(c["page"], s["table"], s["lengths"], s["has"], s["free"], s["left"], *s["spare"])
         return s["table"], s["lengths"], s["left"], s["free"], s["offsets"], s["maps"], s["status"]
     if c["op"] == "prefix":
         api.mxattn_prefix_run(h["cache"], fmt[c["type"]], s["q"], s["out"], s["table"], s["lengths"], s["longest"], s["first"], s["shared"],
