@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmxgemm.so")
 
 MX_E4M3, MX_E5M2, MX_E2M3, MX_E3M2, MX_E2M1, MX_E8M0, MX_F16, MX_INT8, MX_INT4 = 0, 1, 2, 3, 4, 8, 16, 32, 33
-MX_BF16, MX_F32 = 17, 18  # rotary positions and the key-value cache only
+MX_BF16, MX_F32 = 17, 18  # not for the block-scaled GEMM, matvec and codecs
 MXGEMM_RELU = 1  # mxgemm_create flag: C = max(A*B, 0) in the epilogue
 MXGEMM_QUANT_A = 2  # mxgemm_create flag: A is binary16, quantised to E4M3 inside the GEMM
 MX_OK, MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT, MX_ERR_ARCH, MX_ERR_LAUNCH, MX_ERR_NOMEM = \
@@ -23,6 +23,8 @@ MX_ERR_SCRATCH = -8
 MXROPE_HALF, MXROPE_PAIRS = 0, 1  # which elements a rotation pairs
 MXROPE_PLAIN, MXROPE_LINEAR, MXROPE_NTK, MXROPE_BANDS, MXROPE_YARN = range(5)  # frequency rules
 MXKV_HEADS_FIRST, MXKV_SLOTS_FIRST = 0, 1  # order of a page's elements
+MXGEMM_I8_MAX_K = 131071
+MXKV_STEP_PAGES, MXKV_STEP_TOKENS, MXKV_STEP_LONG, MXKV_STEP_STACK = 1, 2, 4, 8  # bits of mxkv_step_run's status
 MXMATVEC_SCRATCH_BYTES = 17 << 20  # static scratch of mxmatvec_run_noalloc, per GPU
 
 if not os.path.exists(LIB_PATH):
@@ -91,6 +93,11 @@ EXPORTS = {
     "mxkv_append_run": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mxattn_decode_run": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
     "mxattn_decode_workspace_size": (ctypes.c_size_t, [_vp, _i, _i, _i, _i]),
+    "mxnorm_run": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, ctypes.c_float, _i, _vp, _vp, _vp]),
+    "mxquant_rows_run": (_i, [_i, _i, _i, _vp, _i, _vp, _vp, _vp]),
+    "mxgemm_i8_run": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _u, _vp, ctypes.c_size_t, _vp]),
+    "mxgemm_i8_workspace_size": (ctypes.c_size_t, [_i, _i, _i]),
+    "mxkv_step_run": (_i, [_vp, _vp]),
     "mxkv_copy_run": (_i, [_vp, _i, _vp, _i, _vp]),
     "mxkv_pool_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i]),
     "mxkv_pool_destroy": (_i, [_vp]),
@@ -374,6 +381,48 @@ def mxkv_copy_run(caches, pairs, stream=None) -> None:
     s = (_marshal or _load()).copy(ctypes.addressof(arr), arr.count, pairs, None if stream is None else _stream(stream), arr.host)
     if s:
         raise MXError(s, "mxkv_copy_run")
+
+
+# ---- 8-bit activations ----------------------------------------------------------------------------
+
+def mxnorm_run(f: int, x, out, scales, fmt: int, weight=None, eps: float = 1e-6, residual=None, total=None, stream=None) -> None:
+    """x, residual, total: [rows][dim] of type f; out: [rows][dim] of fmt (f, or bytes); weight: [dim]; scales: fp32 [rows] for
+    MX_INT8, bytes [rows][dim / 32] for MX_E4M3 and MX_E5M2, None for f."""
+    s = (_marshal or _load()).norm(f, x, out, scales, fmt, weight, eps, residual, total, None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxnorm_run")
+
+
+def mxquant_rows_run(f: int, x, out, scales, fmt: int, stream=None) -> None:
+    """x: [rows][dim] of type f; out, scales: as for mxnorm_run."""
+    s = (_marshal or _load()).quant(f, x, out, scales, fmt, None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxquant_rows_run")
+
+
+def mxgemm_i8_workspace_size(M: int, N: int, K: int) -> int:
+    _ints("mxgemm_i8_workspace_size", M, N, K)
+    return int(_lib.mxgemm_i8_workspace_size(M, N, K))
+
+
+def mxgemm_i8_run(A, SA, B, SB, C, fc: int, bias=None, flags: int = 0, workspace=None, workspace_bytes=None, stream=None) -> None:
+    """A: int8 [M][K], SA: fp32 [M]; B: int8 [N][K], SB: fp32 [N]; C: [M][N] and bias: [N] of type fc; workspace: a zero-filled device
+    buffer (a tensor's own size when workspace_bytes is omitted)."""
+    s = (_marshal or _load()).gemm_i8(A, SA, B, SB, C, fc, bias, flags, workspace, workspace_bytes, None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxgemm_i8_run")
+
+
+# ---- a step's pages and tokens on the device -----------------------------------------------------
+
+def mxkv_step_run(page_size: int, table, lengths, wants, free, n_free, offsets, seq, positions, slots, status, kept=None,
+                  lengths_out=None, n_free_out=None, stream=None) -> None:
+    """All int32: table [seqs][cols]; lengths, wants, kept [seqs]; free [pages]; n_free, status [1]; offsets [seqs + 1]; seq,
+    positions, slots [max_tokens]. lengths_out and n_free_out: lengths and n_free themselves when omitted."""
+    s = (_marshal or _load()).step(page_size, table, lengths, wants, free, n_free, offsets, seq, positions, slots, status, kept,
+                                   lengths_out, n_free_out, None if stream is None else _stream(stream))
+    if s:
+        raise MXError(s, "mxkv_step_run")
 
 
 class KVPool:

@@ -224,6 +224,165 @@ int copy(PyObject* const* a) {
   return unlocked([&] { return mxkv_copy_run(layers, n_layers, pairs, n, stream); });
 }
 
+// A [rows][dim] tensor, dim contiguous. False: another shape.
+bool matrix(const at::Tensor& t, mx_rows* m) {
+  if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1) || !is_int(t.size(0)) || !is_int(t.size(1))) return false;
+  // a single row has no stride of its own: that of its whole 16-byte pieces
+  const int64_t unit = 16 / t.element_size(), whole = (t.size(1) + unit - 1) / unit * unit;
+  *m = mx_rows{t.data_ptr(), t.size(0) > 1 ? t.stride(0) : whole};
+  return true;
+}
+
+// Whether a dense tensor of this type and shape stands here; None: NULL.
+template <typename T>
+bool dense(PyObject* o, at::IntArrayRef shape, at::ScalarType type, T** p) {
+  *p = nullptr;
+  if (o == Py_None) return true;
+  const at::Tensor& t = tensor(o);
+  if (t.scalar_type() != type || t.sizes() != shape || !t.is_contiguous()) return false;
+  *p = static_cast<T*>(t.data_ptr());
+  return true;
+}
+
+// A workspace (tensor, address or None) and its size, None: the tensor's own. False: a size that the tensor does not have.
+bool workspace_of(PyObject* o, PyObject* size, void** p, size_t* bytes) {
+  *bytes = 0;
+  if (THPVariable_Check(o)) {
+    const at::Tensor& t = tensor(o);
+    if (!t.is_contiguous()) return false;
+    *p = t.data_ptr(), *bytes = t.nbytes();
+  } else {
+    *p = address<void>(o);
+  }
+  if (size == Py_None) return true;
+  const int64_t given = integer(size);
+  if (given < 0 || (THPVariable_Check(o) && (size_t)given > *bytes)) return false;
+  *bytes = (size_t)given;
+  return true;
+}
+
+at::ScalarType type_of(int f) { return f == MX_F32 ? at::kFloat : f == MX_BF16 ? at::kBFloat16 : at::kHalf; }
+
+// Bytes that stand for format f: of its type, or whole numbers of 8 bits.
+bool holds(const at::Tensor& t, int f) {
+  const at::ScalarType s = t.scalar_type();
+  if (f == MX_F16 || f == MX_BF16 || f == MX_F32) return s == type_of(f);
+  if (t.element_size() != 1 || s == at::kBool) return false;
+  return !at::isFloatingType(s) || (f == MX_E4M3 && s == at::kFloat8_e4m3fn) || (f == MX_E5M2 && s == at::kFloat8_e5m2);
+}
+
+// The scales of rows in fmt, as norm and quantisation write them.
+int scales_of(PyObject* o, int fmt, const at::Tensor& out, void** p) {
+  *p = nullptr;
+  if (o == Py_None) return MX_OK;
+  const at::Tensor& t = tensor(o);
+  const bool block = fmt == MX_E4M3 || fmt == MX_E5M2;
+  if (!t.is_contiguous() || t.dim() != (block ? 2 : 1) || t.size(0) != out.size(0) || (block && t.size(1) != out.size(1) / 32)) return MX_ERR_SHAPE;
+  if (block ? t.element_size() != 1 || (at::isFloatingType(t.scalar_type()) && t.scalar_type() != at::kFloat8_e8m0fnu) : t.scalar_type() != at::kFloat)
+    return MX_ERR_FORMAT;
+  *p = t.data_ptr();
+  return MX_OK;
+}
+
+// (f, x, out, scales, fmt, weight, eps, residual, total, stream)
+int norm(PyObject* const* a) {
+  const int f = narrow(a[0], MX_ERR_FORMAT), fmt = narrow(a[4], MX_ERR_FORMAT);
+  const at::Tensor &x = tensor(a[1]), &out = tensor(a[2]);
+  mx_rows m[4];
+  const int place[4] = {1, 2, 7, 8};
+  for (int i = 0; i < 4; i++) {
+    if (a[place[i]] == Py_None) continue;
+    const at::Tensor& t = tensor(a[place[i]]);
+    if (!matrix(t, &m[i]) || t.sizes() != x.sizes()) return MX_ERR_SHAPE;
+    if (!holds(t, i == 1 ? fmt : f)) return MX_ERR_FORMAT;
+  }
+  void *scales, *weight = nullptr;
+  if (int s = scales_of(a[3], fmt, out, &scales)) return s;
+  if (a[5] != Py_None) {
+    const at::Tensor& t = tensor(a[5]);
+    if (!holds(t, f)) return MX_ERR_FORMAT;
+    if (t.dim() != 1 || t.size(0) != x.size(1) || !t.is_contiguous()) return MX_ERR_SHAPE;
+    weight = t.data_ptr();
+  }
+  const float eps = (float)number(a[6]);
+  on_gpu(Py_False, {a[1], a[2], a[3], a[5], a[7], a[8]});
+  void* stream = stream_of(a[9]);
+  return unlocked([&] {
+    return mxnorm_run(f, (int)x.size(0), (int)x.size(1), &m[0], a[7] == Py_None ? nullptr : &m[2], a[8] == Py_None ? nullptr : &m[3], weight, eps, fmt,
+                      &m[1], scales, stream);
+  });
+}
+
+// (f, x, out, scales, fmt, stream)
+int quant(PyObject* const* a) {
+  const int f = narrow(a[0], MX_ERR_FORMAT), fmt = narrow(a[4], MX_ERR_FORMAT);
+  const at::Tensor &x = tensor(a[1]), &out = tensor(a[2]);
+  mx_rows mx, mo;
+  if (!matrix(x, &mx) || !matrix(out, &mo) || out.sizes() != x.sizes()) return MX_ERR_SHAPE;
+  if (!holds(x, f) || !holds(out, fmt)) return MX_ERR_FORMAT;
+  void* scales;
+  if (int s = scales_of(a[3], fmt, out, &scales)) return s;
+  on_gpu(Py_False, {a[1], a[2], a[3]});
+  void* stream = stream_of(a[5]);
+  return unlocked([&] { return mxquant_rows_run(f, (int)x.size(0), (int)x.size(1), &mx, fmt, &mo, scales, stream); });
+}
+
+// Whether every row's last 16-byte piece lies within the tensor's memory.
+bool whole_pieces(const at::Tensor& t, const mx_rows& m) {
+  if (t.numel() == 0) return true;
+  const int64_t last = t.storage_offset() + (t.size(0) - 1) * m.stride + (t.size(1) + 15) / 16 * 16;
+  return last <= (int64_t)t.storage().nbytes();
+}
+
+// (A, SA, B, SB, C, fc, bias, flags, workspace, workspace_bytes, stream)
+int gemm_i8(PyObject* const* a) {
+  const at::Tensor &A = tensor(a[0]), &B = tensor(a[2]), &C = tensor(a[4]);
+  const int fc = narrow(a[5], MX_ERR_FORMAT);
+  const int64_t flags = integer(a[7]);
+  mx_rows ma, mb, mc;
+  if (!matrix(A, &ma) || !matrix(B, &mb) || !matrix(C, &mc)) return MX_ERR_SHAPE;
+  if (A.size(1) != B.size(1) || C.size(0) != A.size(0) || C.size(1) != B.size(0)) return MX_ERR_SHAPE;
+  if (!holds(A, MX_INT8) || !holds(B, MX_INT8) || A.scalar_type() == at::kByte || B.scalar_type() == at::kByte) return MX_ERR_FORMAT;
+  if ((fc != MX_F16 && fc != MX_BF16 && fc != MX_F32) || !holds(C, fc) || flags < 0 || flags > INT_MAX) return MX_ERR_FORMAT;
+  if (!whole_pieces(A, ma) || !whole_pieces(B, mb)) return MX_ERR_SHAPE;
+  float *sa, *sb;
+  void *bias, *workspace;
+  size_t bytes;
+  if (!dense(a[1], A.sizes().slice(0, 1), at::kFloat, &sa) || !dense(a[3], B.sizes().slice(0, 1), at::kFloat, &sb)) return MX_ERR_SHAPE;
+  if (a[6] != Py_None && !holds(tensor(a[6]), fc)) return MX_ERR_FORMAT;
+  if (!dense(a[6], B.sizes().slice(0, 1), type_of(fc), &bias) || !workspace_of(a[8], a[9], &workspace, &bytes)) return MX_ERR_SHAPE;
+  on_gpu(Py_False, {a[0], a[1], a[2], a[3], a[4], a[6], a[8]});
+  void* stream = stream_of(a[10]);
+  return unlocked([&] {
+    return mxgemm_i8_run((int)A.size(0), (int)B.size(0), (int)A.size(1), &ma, sa, &mb, sb, bias, fc, &mc, (unsigned)flags, workspace, bytes, stream);
+  });
+}
+
+// (page_size, table, lengths, wants, free, n_free, offsets, seq, positions, slots, status, kept, lengths_out, n_free_out, stream)
+int step(PyObject* const* a) {
+  mxkv_step s = {};
+  const at::Tensor &table = tensor(a[1]), &free = tensor(a[4]);
+  if (table.dim() != 2 || table.scalar_type() != at::kInt || !table.is_contiguous() || !is_int(table.size(0)) || !is_int(table.size(1))) return MX_ERR_SHAPE;
+  if (free.dim() != 1 || !is_int(free.size(0))) return MX_ERR_SHAPE;
+  const int64_t n = table.size(0), more = n + 1, one = 1;
+  const int64_t room = a[7] == Py_None ? 0 : tensor(a[7]).numel();
+  if (!is_int(room)) return MX_ERR_SHAPE;
+  s.seqs = (int)n, s.cols = (int)table.size(1), s.page_size = narrow(a[0], MX_ERR_SHAPE), s.pages = (int)free.size(0), s.max_tokens = (int)room;
+  s.table = static_cast<int32_t*>(table.data_ptr());
+  int32_t *lengths, *wants, *kept, *n_free;
+  if (!dense(a[2], {n}, at::kInt, &lengths) || !dense(a[3], {n}, at::kInt, &wants) || !dense(a[11], {n}, at::kInt, &kept) ||
+      !dense(a[4], free.sizes(), at::kInt, &s.free_pages) || !dense(a[5], {one}, at::kInt, &n_free) || !dense(a[6], {more}, at::kInt, &s.offsets) ||
+      !dense(a[7], {room}, at::kInt, &s.seq) || !dense(a[8], {room}, at::kInt, &s.positions) || !dense(a[9], {room}, at::kInt, &s.slots) ||
+      !dense(a[10], {one}, at::kInt, &s.status) || !dense(a[12], {n}, at::kInt, &s.lengths_out) || !dense(a[13], {one}, at::kInt, &s.n_free_out))
+    return MX_ERR_SHAPE;
+  s.lengths = lengths, s.wants = wants, s.kept = kept, s.n_free = n_free;
+  if (!s.lengths_out) s.lengths_out = lengths;
+  if (!s.n_free_out) s.n_free_out = n_free;
+  on_gpu(Py_False, {a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12], a[13]});
+  void* stream = stream_of(a[14]);
+  return unlocked([&] { return mxkv_step_run(&s, stream); });
+}
+
 template <int (*F)(PyObject* const*), int COUNT>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t count) {
   if (count != COUNT) {
@@ -249,6 +408,7 @@ constexpr PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<rope, 8>("rope"), method<append, 12>("append"), method<attention, 16>("attention"), method<copy, 5>("copy"),
+                         method<norm, 10>("norm"), method<quant, 6>("quant"), method<gemm_i8, 11>("gemm_i8"), method<step, 15>("step"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -30,7 +30,7 @@
  *  - Scales of MX operands: E8M0 bytes, value 2^(e-127), 0xFF = NaN; one scale per 32
  *    consecutive elements along K ("Scale planes: one MTLTensor = data + scales" and the
  *    auxiliary-plane blockFactors {32,1} of the WWDC26 session 330 summary).
- *  - MX_BF16: bfloat16, and MX_F32: binary32 (rotary positions and the key-value cache only).
+ *  - MX_BF16: bfloat16, and MX_F32: binary32 (not for the block-scaled GEMM, matvec and codecs).
  *  - MX_F16: IEEE binary16. MX_INT8: two's-complement bytes. MX_INT4: two's-complement nibbles,
  *    packed two per byte along the C-order linear index, the even index in the low nibble
  *    ("TensorOps ... notes", section "VALIDATED ON M4 MAX", fact 5).
@@ -289,6 +289,62 @@ uint8_t mx_encode_host(int f, float v);
 float mx_decode_host(int f, uint8_t code);
 
 /* ------------------------------------------------------------------------------------------ */
+/* 8-bit activations: the norm before them, the product of 8-bit integers.                      */
+/* ------------------------------------------------------------------------------------------ */
+
+/* A matrix of rows with their elements contiguous, one every `stride` elements, each row 16-byte aligned. */
+typedef struct {
+  void* data;
+  int64_t stride;
+} mx_rows;
+
+/*
+ * mxnorm_run -- root-mean-square norm of rows, with the residual's addition before it:
+ *   h = x + residual, rounded to f (residual NULL: h = x);  y_i = h_i weight_i / sqrt(mean_j h_j^2 + eps).
+ *  - f: MX_F16, MX_BF16 or MX_F32 (x, residual, total, weight). total (NULL: not wanted; needs a residual) receives h and may be
+ *    x or residual itself. weight: [dim] (NULL: ones).
+ *  - fmt: what y is written as. f: y rounded, scales unused. MX_INT8: out bytes q = rint(127 y / max|y|) of the row, ties to
+ *    even, and scales, fp32 [rows], max|y| / 127, for mxgemm_i8_run; a row of zeros has scale 0, a row with an infinity
+ *    or NaN scale NaN and zeros. MX_E4M3 and MX_E5M2 (dim % 32 == 0): the codes and E8M0 scales, [rows][dim / 32], that mx_pack_run's rule
+ *    gives y, for mxgemm_run (which wants out->stride == dim).
+ *  - Squares are summed and y is formed in fp32, and rounded once. Rows whose squares pass fp32's range (or vanish in it) are
+ *    scaled by a power of two first, so every finite row has its norm.
+ * 1 <= dim <= MX_MAX_DIM, 0 <= rows <= MX_MAX_DIM (0: nothing is done); strides at least dim, in multiples of 16 bytes; eps finite and
+ * not negative. Besides total, outputs must not overlap inputs. Elements between dim and the stride are neither
+ * read nor written.
+ */
+int mxnorm_run(int f, int rows, int dim, const mx_rows* x, const mx_rows* residual, const mx_rows* total, const void* weight, float eps,
+               int fmt, const mx_rows* out, void* scales, void* stream);
+
+/* mxquant_rows_run -- the same outputs of x as it is, without a norm: activations that no norm precedes, or a weight
+ * [N][K] by output channel. fmt: MX_INT8, MX_E4M3 or MX_E5M2. */
+int mxquant_rows_run(int f, int rows, int dim, const mx_rows* x, int fmt, const mx_rows* out, void* scales, void* stream);
+
+/* Largest K of mxgemm_i8_run: sums of K products of 8-bit integers fit 32 bits. */
+#define MXGEMM_I8_MAX_K 131071
+
+/*
+ * mxgemm_i8_run -- C[m,n] = SA[m] SB[n] sum_k A[m,k] B[n,k] (+ bias[n]): the product of 8-bit integers with one scale per
+ * row of A (token) and one per row of B (output channel).
+ *   A int8 [M][K], SA fp32 [M]; B int8 [N][K] (K contiguous, as the block-scaled GEMM's), SB fp32 [N]; C [M][N] in fc, MX_F16, MX_BF16 or
+ *   MX_F32; bias [N] in fc (NULL: none); flags: 0 or MXGEMM_RELU (C = max(C, 0), after the bias).
+ * The sum is exact; it, the scales' product and theirs are rounded to fp32, the bias is added, and the result is
+ * rounded to fc. Results are the same bits for every workspace.
+ * 0 <= M <= MX_MAX_DIM (0: nothing is done), 1 <= N <= MX_MAX_DIM, 1 <= K <= MXGEMM_I8_MAX_K, all odd ones among them. Strides: A's and B's at least K and
+ * multiples of 16, at most MX_MAX_DIM; C's at least N (rows of C that are not 16-byte aligned are written by
+ * elements). Every row of A and B, the last one too, is read up to the next multiple of 16 bytes past K; what stands there does
+ * not matter.
+ * Workspace as for mxmatvec_run, of mxgemm_i8_workspace_size() bytes, zero-filled before its first use and left reusable by every
+ * call, of this or other shapes: where there are few tiles, workgroups split K and their sums meet there. Calls that may overlap in time need separate
+ * workspaces. Without one, or with too small a one, K is not split.
+ */
+int mxgemm_i8_run(int M, int N, int K, const mx_rows* A, const float* SA, const mx_rows* B, const float* SB, const void* bias, int fc,
+                  const mx_rows* C, unsigned flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes mxgemm_i8_run uses for these sizes (0: none needed, or invalid sizes). */
+size_t mxgemm_i8_workspace_size(int M, int N, int K);
+
+/* ------------------------------------------------------------------------------------------ */
 /* The decode step's cache: rotary positions, a paged key-value cache, attention over it.       */
 /* ------------------------------------------------------------------------------------------ */
 
@@ -435,6 +491,45 @@ size_t mxattn_decode_workspace_size(const mxkv_cache* cache, int seqs, int q_hea
  * nothing is done). MX_ERR_SHAPE also where the layers' geometry differs, and for pages of 16 GiB of keys and more.
  */
 int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32_t* pairs, int n_pairs, void* stream);
+
+/* Why mxkv_step_run did nothing (bits of its status): too few free pages; more new tokens than max_tokens; a row longer than its
+ * table's columns; pages given back that would overfill the stack, which then did not hold what was free. */
+#define MXKV_STEP_PAGES 1
+#define MXKV_STEP_TOKENS 2
+#define MXKV_STEP_LONG 4
+#define MXKV_STEP_STACK 8
+
+/*
+ * mxkv_step_run -- a step's page tables, tokens and slots from the rows' lengths, on the device (the pool below is the same on the
+ * host, and knows shared pages). Row b has lengths[b] tokens in the cache and is to have wants[b] (negative: as
+ * many as it has). All pointers are to device memory.
+ *  - A row that grows takes pages for its columns from the end of free_pages[0 .. *n_free - 1]; one that shrinks gives its last pages
+ *    back there, those of columns below kept[b] apart (kept NULL: 0), which it shares and does not own. Cells of the table that lose
+ *    their page become -1. Pages are given back before any is taken, rows in order, columns in order; giving back what a call took
+ *    restores the stack.
+ *  - The step's tokens, positions lengths[b] .. wants[b] - 1 of every row that grows, rows in order: token t has row seq[t],
+ *    position positions[t], and slots[t] = page * page_size + position % page_size (slots NULL: not wanted; -1 without
+ *    a page). Row b's tokens are offsets[b] .. offsets[b + 1] - 1. seq, positions and slots of the places behind the last token, to
+ *    max_tokens, become -1: mxkv_append_run leaves such tokens out, so a captured step may have fewer.
+ *  - lengths_out = the new lengths and *n_free_out (each may be what it was read from), *status = 0. Where the step is not
+ *    possible, *status is a sum of MXKV_STEP_ bits, lengths and n_free are copied, the table and the stack stay, and the step
+ *    has no tokens.
+ * lengths outside 0 .. cols * page_size are taken as that bound. A row's cells of the positions that it has are expected
+ * to hold its pages, as calls leave them, and the stack to hold free ones.
+ * Rules (MX_ERR_SHAPE): 0 <= seqs (0: nothing is done), pages, page_size, max_tokens <= MX_MAX_DIM; cols * page_size and pages * page_size below 2^31.
+ */
+typedef struct {
+  int seqs, cols, page_size, pages, max_tokens;
+  int32_t* table;                         /* [seqs][cols] */
+  const int32_t *lengths, *wants, *kept;  /* [seqs] */
+  int32_t* free_pages;                    /* [pages] */
+  const int32_t* n_free;                  /* [1] */
+  int32_t *lengths_out, *n_free_out;      /* [seqs], [1] */
+  int32_t *offsets;                       /* [seqs + 1] */
+  int32_t *seq, *positions, *slots;       /* [max_tokens] */
+  int32_t* status;                        /* [1] */
+} mxkv_step;
+int mxkv_step_run(const mxkv_step* step, void* stream);
 
 /*
  * mxkv_pool -- host bookkeeping of a cache's pages: which page belongs to which sequences, as tables
