@@ -93,6 +93,8 @@ EXPORTS = {
     "mxkv_append_run": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mxattn_decode_run": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
     "mxattn_decode_workspace_size": (ctypes.c_size_t, [_vp, _i, _i, _i, _i]),
+    "mxattn_prefix_run": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
+    "mxattn_prefix_workspace_size": (ctypes.c_size_t, [_vp, _i, _i, _i, _i, _i]),
     "mxnorm_run": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, ctypes.c_float, _i, _vp, _vp, _vp]),
     "mxquant_rows_run": (_i, [_i, _i, _i, _vp, _i, _vp, _vp, _vp]),
     "mxgemm_i8_run": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _u, _vp, ctypes.c_size_t, _vp]),
@@ -373,6 +375,20 @@ def mxattn_decode_run(cache: KVCache, f: int, q, out, table, lengths, max_len: i
                                         workspace, workspace_bytes, None if stream is None else _stream(stream), cache.host)
     if s:
         raise MXError(s, "mxattn_decode_run")
+
+
+def mxattn_prefix_workspace_size(cache: KVCache, seqs: int, q_heads: int, groups: int, max_len: int, max_shared: int) -> int:
+    _ints("mxattn_prefix_workspace_size", seqs, q_heads, groups, max_len, max_shared)
+    return int(_lib.mxattn_prefix_workspace_size(cache.ref, seqs, q_heads, groups, max_len, max_shared))
+
+
+def mxattn_prefix_run(cache: KVCache, f: int, q, out, table, lengths, max_len: int, first, shared, max_shared: int, scale: float, lse=None,
+                      softcap: float = 0.0, workspace=None, workspace_bytes=None, stream=None) -> None:
+    """As mxattn_decode_run, for groups of rows that share beginnings: first: int32 [groups + 1], shared: int32 [groups]."""
+    s = (_marshal or _load()).prefix(cache.ref, f, q, out, table, lengths, max_len, first, shared, max_shared, scale, lse, softcap, workspace,
+                                     workspace_bytes, None if stream is None else _stream(stream), cache.host)
+    if s:
+        raise MXError(s, "mxattn_prefix_run")
 
 
 def mxkv_copy_run(caches, pairs, stream=None) -> None:

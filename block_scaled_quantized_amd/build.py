@@ -23,7 +23,7 @@ MARSHAL = os.path.join(HERE, "_marshal.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "host_codec.cpp", "codec.hip", "mxgemm.hip", "mxgemm_ring.hip", "matvec.hip",
-           "rotary.hip", "attention.hip", "pages.hip", "page_pool.cpp", "norm.hip", "gemm_i8.hip", "step.hip"]
+           "rotary.hip", "attention.hip", "prefix.hip", "pages.hip", "page_pool.cpp", "norm.hip", "gemm_i8.hip", "step.hip"]
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-x", "hip",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wno-unused-command-line-argument", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -28,16 +28,12 @@
 // takes up to 2 us more there, and boxes differ by a tenth.
 #include <algorithm>
 
-#include "kvcache.h"
+#include "attention.h"
 
 using namespace mx;
 
 namespace {
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kTile = 32;                // keys of a wave's tile
@@ -51,7 +47,6 @@ constexpr int kPad = 4;                  // floats that keep the heads' rows of 
 // joins otherwise wait for their instructions (131072 x 8 x 128 fp16: 114 -> 103 us).
 constexpr int kStream = 2;
 constexpr int kFar = 1 << 30;            // a byte offset past every buffer: loads give 0
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct Args {
   const uint8_t *k, *v, *ks, *vs;
@@ -65,47 +60,8 @@ struct Args {
   int seqs, heads, group, tiles, dim, cols, pages, page_size, max_len, max_keys, window, wgs;
   float scale, softcap;
   FastDiv page_div, units_div, tiles_div, wgs_div, quads_div;  // units: of one sequence
+  Prefix prefix;  // shared positions' results, which a row's own are added to
 };
-
-template <typename T>
-struct Vec;
-template <>
-struct Vec<_Float16> {
-  typedef f16x8 x8;
-  // A probability p = 2^(x - m) goes to the matrix cores as two values of T: p cut to T, and what that leaves rounded
-  // to T. Together they hold 21 bits of p (bfloat16: 15). One value alone made the error against 64 bits 1.2 to 1.4
-  // times that of the result's own rounding. The second is never 0 nor negative, as its product with an infinite value has
-  // to be what the first one's is: kLeast, 2^-39 of the largest p (bfloat16: 2^-126), is far below a half step of any sum.
-  // p is at most 1; binary16 would lose those under 2^-24, which can matter in number in a long row, so they
-  // are scaled by 2^15 (which cancels in the division by their sum). bfloat16 has the range.
-  static constexpr float kShift = 15.0f, kLeast = 0x1p-24f;
-  static MX_DEV uint32_t cut(float a, float b) { return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b)); }
-  static MX_DEV f32x4 mfma(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-  template <bool HI>
-  static MX_DEV uint32_t from_e4m3(uint32_t w, float scale) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, HI));
-  }
-};
-template <>
-struct Vec<__bf16> {
-  typedef bf16x8 x8;
-  static constexpr float kShift = 0.0f, kLeast = 0x1p-126f;
-  static MX_DEV uint32_t cut(float a, float b) { return __builtin_amdgcn_perm(fbits(b), fbits(a), 0x07060302u); }
-  static MX_DEV f32x4 mfma(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-  template <bool HI>
-  static MX_DEV uint32_t from_e4m3(uint32_t w, float scale) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, HI));
-  }
-};
-
-// Eight E4M3 codes times 2^(e - 127) as eight 16-bit values: the conversion reads the scale's exponent bits
-// as an E8M0 number, 0 as 2^-127 and 255 as NaN.
-template <typename T>
-MX_DEV u32x4 widen(u32x2 c, uint32_t e) {
-  const float s = bitsf(e << 23);
-  return (u32x4){Vec<T>::template from_e4m3<false>(c[0], s), Vec<T>::template from_e4m3<true>(c[0], s),
-                 Vec<T>::template from_e4m3<false>(c[1], s), Vec<T>::template from_e4m3<true>(c[1], s)};
-}
 
 // Over the four lanes that hold one head (lane % 16): exchanges of rows of 16 and of halves of the wave.
 MX_DEV float wave_max(float x) {
@@ -120,7 +76,6 @@ MX_DEV float wave_sum(float x) {
   r = __builtin_amdgcn_permlane32_swap(fbits(x), fbits(x), false, false);
   return bitsf(r[0]) + bitsf(r[1]);
 }
-MX_DEV float finite_or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
 
 template <typename T>
 MX_DEV void store4(T* p, f32x4 v) {
@@ -275,15 +230,6 @@ MX_DEV Cuts share_of(Kernarg& a, int units, Place& from, Place& to) {
     sum += total;
   }
   return cuts;
-}
-
-// c tanh(s / c): where |s / c| < 0.2 by its series, whose fifth term is below half a step, else by one
-// exponential, whose error is relative to c. A cap that is far above every score leaves them as they are.
-MX_DEV float soft_cap(float s, float c) {
-  const float y = s * fminf(1.0f / c, 3.0e38f), z = y * y;
-  const float near = s * fmaf(z, fmaf(z, fmaf(z, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
-  const float far = fmaf(c, -2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.0f * kLog2e * y)), c);
-  return fabsf(y) < 0.2f ? near : far;
 }
 
 // Tiles of a wave on their way: two, or one of D = 256, whose registers would not hold a second; and one where
@@ -725,6 +671,35 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
     const auto put_lse = [&](int h, float top, float sum) {
       if (z.lse) z.lse[(int64_t)b * z.heads * z.group + first_head + h] = sum == 0.f ? -INFINITY : kLn2 * (top - kShift + __log2f(sum));
     };
+    // The head's results of the positions that its row shares, four splits of them at a time.
+    const auto add_shared = [&](int h, int d, f32x4& o, float& top, float& sum) {
+      if (!z.prefix.partial) return;
+      const i32x4 r = z.prefix.rows[b];
+      const int splits = r[1], head = r[3] + kHeads * ht + h;
+      const int64_t size = prefix_slot_floats(dim);
+      const float* p = z.prefix.partial + (r[0] + (int64_t)(hk * r[2] + head / kPrefixRows) * splits) * size;
+      const int outs = (d * (kPrefixRows / 4) + head % kPrefixRows) * 4, stats = kPrefixRows * dim + 2 * (head % kPrefixRows);
+#pragma unroll 1
+      for (int i = 0; i < splits; i += 4, p += 4 * size) {
+        float m[4], l[4];
+        f32x4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const int64_t at = i + u < splits ? u * size : 0;
+          m[u] = p[at + stats], l[u] = p[at + stats + 1], v[u] = *reinterpret_cast<const f32x4*>(p + at + outs);
+        }
+        float most = fmaxf(top, m[0]);
+#pragma unroll
+        for (int u = 1; u < 4; u++) most = fmaxf(most, m[u]);
+        const float ref = finite_or_zero(most), f = __builtin_amdgcn_exp2f(top - ref);
+        o *= f, sum *= f, top = most;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const float w = i + u < splits ? __builtin_amdgcn_exp2f(m[u] - ref) : 0.f;
+          if (w > 0.f) o += v[u] * w, sum += l[u] * w;
+        }
+      }
+    };
     const bool whole = !SPLIT || (at.grain == 0 && stop == row.grains);
     // Partials, one for a share that begins within a unit and one for a unit that ends past the share:
     // [kHeads][dim] outputs, then [kHeads] {maximum, sum}.
@@ -738,8 +713,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
       f32x4 o = *reinterpret_cast<const f32x4*>(lds + h * kLd + d);
 #pragma unroll
       for (int w = 1; w < kHalf; w++) o += *reinterpret_cast<const f32x4*>(lds + (w * n_heads + h) * kLd + d);
-      const float sum = head_l[h], top = head_m[h];
+      float sum = head_l[h], top = head_m[h];
       if (whole) {
+        add_shared(h, d, o, top, sum);
         finish(h, d, o, sum);
         if (d == 0) put_lse(h, top, sum);
       } else {
@@ -855,8 +831,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
           }
           if (mine && part == 0) {
             float sum;
-            const float top = joined(h, sum);
+            float top = joined(h, sum);
             if (result) {
+              add_shared(h, d, o, top, sum);
               finish(h, d, o, sum);
               if (d == 0) put_lse(h, top, sum);
             } else {
@@ -907,6 +884,7 @@ int workgroups(int D, int fmt, int ht) {
 // Three counters per workgroup, at one place for every call: a workspace that served another shape has its
 // partials past them.
 constexpr size_t kCounterBytes = 3 * 2 * kCUs * 4;
+static_assert(kCounterBytes == kDecodeCounterBytes, "counters");
 
 Plan plan_for(const mxkv_cache* c, int seqs, int q_heads, int max_len, int window) {
   Plan p = {};
@@ -960,29 +938,36 @@ void launch_dim(const Args& a, const Plan& p, bool split, hipStream_t st) {
 
 }  // namespace
 
-extern "C" size_t mxattn_decode_workspace_size(const mxkv_cache* cache, int seqs, int q_heads, int max_len, int window) {
+namespace mx {
+
+bool decode_sizes_ok(const mxkv_cache* cache, int seqs, int q_heads, int max_len, int window) { return sizes_ok(cache, seqs, q_heads, max_len, window); }
+
+size_t decode_workspace(const mxkv_cache* cache, int seqs, int q_heads, int max_len, int window) {
   if (!cache || check_geometry(cache) || !sizes_ok(cache, seqs, q_heads, max_len, window) || seqs == 0) return 0;
   return plan_for(cache, seqs, q_heads, max_len, window).bytes;
 }
 
-extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, float* lse,
-                                 const mxkv_table* table, const int32_t* lengths, const int32_t* starts, int max_len,
-                                 const mxattn_opts* opts, void* workspace, size_t workspace_bytes, void* stream) {
+int check_attention(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, const mxkv_table* table, const int32_t* lengths, int max_len,
+                    const mxattn_opts* opts) {
   if (!cache || !q || !out || !table || !opts) return MX_ERR_NULL;
   if (f != MX_F16 && f != MX_BF16) return MX_ERR_FORMAT;
   if (int s = check_cache(cache)) return s;
-  const bool mx8 = cache->fmt == MX_E4M3;
-  if (!mx8 && cache->fmt != f) return MX_ERR_FORMAT;
+  if (cache->fmt != MX_E4M3 && cache->fmt != f) return MX_ERR_FORMAT;
   if (int s = check_table(table)) return s;
   if (!sizes_ok(cache, table->seqs, q->heads, max_len, opts->window) || q->heads != out->heads) return MX_ERR_SHAPE;
   if (!__builtin_isfinite(opts->scale) || !__builtin_isfinite(opts->softcap) || opts->softcap < 0.f) return MX_ERR_SHAPE;
   if (table->seqs == 0) return MX_OK;
   if (!lengths) return MX_ERR_NULL;
   if (int s = check_heads(q, 2)) return s;
-  if (int s = check_heads(out, 2)) return s;
-  if (workspace && !aligned16(workspace)) return MX_ERR_ALIGN;
+  return check_heads(out, 2);
+}
+
+int decode_launch(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, float* lse, const mxkv_table* table, const int32_t* lengths,
+                  const int32_t* starts, int max_len, const mxattn_opts* opts, const Prefix& prefix, void* workspace, size_t workspace_bytes, hipStream_t st) {
+  const bool mx8 = cache->fmt == MX_E4M3;
   const Plan p = plan_for(cache, table->seqs, q->heads, max_len, opts->window);
   Args a = {};
+  a.prefix = prefix;
   a.k = (const uint8_t*)cache->k, a.v = (const uint8_t*)cache->v;
   a.ks = (const uint8_t*)cache->ks, a.vs = (const uint8_t*)cache->vs;
   a.q = q->data, a.qt = q->token_stride, a.qh = q->head_stride;
@@ -1005,11 +990,26 @@ extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads*
   a.tiles_div = FastDiv((uint32_t)p.tiles);
   a.wgs_div = FastDiv((uint32_t)(split ? p.wgs : 1));
   a.quads_div = FastDiv((uint32_t)cache->dim / 4);
-  if (int s = check_arch()) return s;
-  const hipStream_t st = as_stream(stream);
   if (f == MX_F16 && mx8) launch_dim<_Float16, true>(a, p, split, st);
   else if (f == MX_F16) launch_dim<_Float16, false>(a, p, split, st);
   else if (mx8) launch_dim<__bf16, true>(a, p, split, st);
   else launch_dim<__bf16, false>(a, p, split, st);
-  return sync_check(launch_status(), st);
+  return launch_status();
+}
+
+}  // namespace mx
+
+extern "C" size_t mxattn_decode_workspace_size(const mxkv_cache* cache, int seqs, int q_heads, int max_len, int window) {
+  return decode_workspace(cache, seqs, q_heads, max_len, window);
+}
+
+extern "C" int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, float* lse,
+                                 const mxkv_table* table, const int32_t* lengths, const int32_t* starts, int max_len,
+                                 const mxattn_opts* opts, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int s = check_attention(cache, f, q, out, table, lengths, max_len, opts)) return s;
+  if (table->seqs == 0) return MX_OK;
+  if (workspace && !aligned16(workspace)) return MX_ERR_ALIGN;
+  if (int s = check_arch()) return s;
+  const hipStream_t st = as_stream(stream);
+  return sync_check(decode_launch(cache, f, q, out, lse, table, lengths, starts, max_len, opts, Prefix{}, workspace, workspace_bytes, st), st);
 }

@@ -261,6 +261,34 @@ bool workspace_of(PyObject* o, PyObject* size, void** p, size_t* bytes) {
   return true;
 }
 
+// (cache, f, q, out, table, lengths, max_len, first, shared, max_shared, scale, lse, softcap, workspace, workspace_bytes, stream, host)
+int prefix(PyObject* const* a) {
+  const mxkv_cache* cache = address<mxkv_cache>(a[0]);
+  const at::Tensor &q = tensor(a[2]), &out = tensor(a[3]), &first = tensor(a[7]), &shared = tensor(a[8]);
+  mx_heads hq, ho;
+  mxkv_table table;
+  mxattn_groups groups;
+  if (!heads(q, &hq) || !heads(out, &ho) || q.sizes() != out.sizes() || q.size(2) != cache->dim) return MX_ERR_SHAPE;
+  const int64_t n = q.size(0);
+  const int32_t* lengths;
+  if (!table_of(a[4], &table) || table.seqs != n || !ints(a[5], {n}, &lengths)) return MX_ERR_SHAPE;
+  if (shared.dim() != 1 || !is_int(shared.size(0)) || !ints(a[7], {shared.size(0) + 1}, &groups.first) || !ints(a[8], shared.sizes(), &groups.shared))
+    return MX_ERR_SHAPE;
+  groups.count = (int)shared.size(0), groups.max_shared = narrow(a[9], MX_ERR_SHAPE);
+  float* lse;
+  void* workspace;
+  size_t bytes;
+  if (!dense(a[11], q.sizes().slice(0, 2), at::kFloat, &lse) || !workspace_of(a[13], a[14], &workspace, &bytes)) return MX_ERR_SHAPE;
+  const int f = narrow(a[1], MX_ERR_FORMAT), max_len = narrow(a[6], MX_ERR_SHAPE);
+  if (!fits(q, f) || !fits(out, f)) return MX_ERR_FORMAT;
+  const mxattn_opts opts = {(float)number(a[10]), (float)number(a[12]), 0};
+  on_gpu(a[16], {a[2], a[3], a[4], a[5], a[7], a[8], a[11], a[13]});
+  void* stream = stream_of(a[15]);
+  return unlocked([&] {
+    return mxattn_prefix_run(cache, f, &hq, &ho, lse, &table, lengths, &groups, max_len, &opts, workspace, bytes, stream);
+  });
+}
+
 at::ScalarType type_of(int f) { return f == MX_F32 ? at::kFloat : f == MX_BF16 ? at::kBFloat16 : at::kHalf; }
 
 // Bytes that stand for format f: of its type, or whole numbers of 8 bits.
@@ -408,7 +436,7 @@ constexpr PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<rope, 8>("rope"), method<append, 12>("append"), method<attention, 16>("attention"), method<copy, 5>("copy"),
-                         method<norm, 10>("norm"), method<quant, 6>("quant"), method<gemm_i8, 11>("gemm_i8"), method<step, 15>("step"),
+                         method<norm, 10>("norm"), method<quant, 6>("quant"), method<gemm_i8, 11>("gemm_i8"), method<step, 15>("step"), method<prefix, 17>("prefix"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -482,6 +482,34 @@ int mxattn_decode_run(const mxkv_cache* cache, int f, const mx_heads* q, const m
  * the geometry of `cache` is read. */
 size_t mxattn_decode_workspace_size(const mxkv_cache* cache, int seqs, int q_heads, int max_len, int window);
 
+/* Rows of a batch whose first positions are the same (a common prompt): group g is the sequences first[g] .. first[g + 1] - 1, which
+ * share their positions below shared[g]. first: int32 [count + 1], not falling, and shared: int32 [count], on the device;
+ * sequences before first[0] and from first[count] on share nothing. max_shared bounds shared (larger ones are taken as it). */
+typedef struct {
+  const int32_t *first, *shared;
+  int count, max_shared;
+} mxattn_groups;
+
+/*
+ * mxattn_prefix_run -- mxattn_decode_run for a batch whose rows share long beginnings: the same results, but a group's shared keys
+ * and values are read once for all of its rows, through the table row of its first sequence. Each row's table still names all of
+ * its pages, as after mxkv_pool_fork; lengths count all positions, the shared ones among them.
+ *  - What is shared is cut to the group's shortest row that has positions, and to whole tiles of 64; a row's other positions are read through
+ *    its own table row. A group with one row that has positions shares nothing.
+ *  - There is no window (opts->window: 0) and there are no starts. Other rules, and the treatment of missing pages, empty rows and lse, are
+ *    mxattn_decode_run's; 0 <= count <= 1024, max_shared >= 0 (MX_ERR_SHAPE).
+ *  - Results are the same up to fp32 summation order.
+ * Workspace as for mxattn_decode_run, of mxattn_prefix_workspace_size() bytes (the buffers of the two are interchangeable where large enough). Without one, or with too small a one,
+ * nothing is shared: every row is read by itself.
+ */
+int mxattn_prefix_run(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, float* lse, const mxkv_table* table,
+                      const int32_t* lengths, const mxattn_groups* groups, int max_len, const mxattn_opts* opts, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Workspace bytes mxattn_prefix_run uses for these sizes (0: none needed, or invalid arguments); only the geometry
+ * of `cache` is read. */
+size_t mxattn_prefix_workspace_size(const mxkv_cache* cache, int seqs, int q_heads, int groups, int max_len, int max_shared);
+
 /*
  * mxkv_copy_run -- copy whole pages (keys, values and scales) of n_layers caches of one geometry, which
  * may be different allocations: page pairs[i][0] to page pairs[i][1] for every i < n_pairs, in every

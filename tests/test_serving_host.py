@@ -162,3 +162,53 @@ def test_binding_refusals_of_the_step():
     refused(api.MX_ERR_SHAPE, run, page_size=1 << 33)
     with pytest.raises(TypeError):
         run()
+
+
+def cache_of(fmt=api.MX_F16, pages=8, page=16, heads=2, dim=64):
+    k = torch.zeros(pages, heads, page, dim, dtype=torch.float16)
+    return api.KVCache(fmt, k, k)
+
+
+class Groups(ctypes.Structure):
+    _fields_ = [("first", ctypes.c_void_p), ("shared", ctypes.c_void_p), ("count", ctypes.c_int), ("max_shared", ctypes.c_int)]
+
+
+def prefix(groups=(P, P, 2, 100), f=api.MX_F16, heads=4, max_len=128, window=0, softcap=0.0, scale=1.0, seqs=3, lengths=P, ws=None, table=P, dim=64):
+    c = cache_of(dim=dim)
+    q = api._Heads(P, heads, heads * dim, dim)
+    t, o = api._Table(table, seqs, 8), api._AttnOpts(scale, softcap, window)
+    g = None if groups is None else ctypes.byref(Groups(*groups))
+    return lib.mxattn_prefix_run(ctypes.byref(c.c), f, ctypes.byref(q), ctypes.byref(q), None, ctypes.byref(t), lengths, g, max_len, ctypes.byref(o), ws, 0, None)
+
+
+@pytest.mark.parametrize("status,args", [
+    (api.MX_ERR_NULL, dict(groups=None)), (api.MX_ERR_NULL, dict(groups=(None, P, 2, 100))), (api.MX_ERR_NULL, dict(groups=(P, None, 2, 100))),
+    (api.MX_ERR_SHAPE, dict(groups=(P, P, -1, 100))), (api.MX_ERR_SHAPE, dict(groups=(P, P, 1025, 100))), (api.MX_ERR_SHAPE, dict(groups=(P, P, 2, -1))),
+    (api.MX_ERR_SHAPE, dict(window=16)), (api.MX_ERR_SHAPE, dict(max_len=0)), (api.MX_ERR_SHAPE, dict(heads=3)), (api.MX_ERR_SHAPE, dict(softcap=-1.0)),
+    (api.MX_ERR_SHAPE, dict(scale=float("nan"))), (api.MX_ERR_FORMAT, dict(f=api.MX_BF16)), (api.MX_ERR_FORMAT, dict(f=api.MX_F32)), (api.MX_ERR_NULL, dict(lengths=None)),
+    (api.MX_ERR_NULL, dict(table=None)), (api.MX_ERR_ALIGN, dict(ws=P + 8)), (api.MX_OK, dict(seqs=0, table=None)),
+])
+def test_prefix_refusals(status, args):
+    assert prefix(**args) == status
+
+
+def test_prefix_workspace_sizes():
+    size, c = api.mxattn_prefix_workspace_size, cache_of()
+    assert size(c, 0, 4, 2, 100, 100) == size(c, 3, 3, 2, 100, 100) == size(c, 3, 4, -1, 100, 100) == size(c, 3, 4, 1025, 100, 100) == size(c, 3, 4, 2, 100, -1) == 0
+    for args in ((1, 4, 1, 5000, 5000), (9, 4, 0, 5000, 5000), (9, 4, 2, 5000, 63), (9, 4, 2, 63, 5000)):  # nothing to share
+        assert size(c, *args) == api.mxattn_decode_workspace_size(c, *args[:2], args[3])
+    assert size(c, 9, 4, 2, 5000, 64) > api.mxattn_decode_workspace_size(c, 9, 4, 5000)
+    with pytest.raises(api.MXError):
+        size(c, 9, 4, 2, 1 << 40, 64)
+
+
+def test_binding_refusals_of_the_prefix():
+    i = lambda *shape: torch.zeros(shape, dtype=torch.int32)  # noqa: E731
+    base = dict(cache=cache_of(), f=api.MX_F16, q=t(3, 4, 64), out=t(3, 4, 64), table=i(3, 8), lengths=i(3), max_len=100, first=i(3), shared=i(2), max_shared=50, scale=1.0)
+    run = lambda **kw: api.mxattn_prefix_run(**{**base, **kw})  # noqa: E731
+    for bad in (dict(out=t(3, 5, 64)), dict(q=t(3, 4, 32), out=t(3, 4, 32)), dict(table=i(2, 8)), dict(lengths=i(4)), dict(first=i(2)), dict(first=i(3).long()),
+                dict(shared=i(2, 1)), dict(max_shared=1 << 31), dict(max_len=1 << 40), dict(lse=t(3, 4)), dict(workspace=t(8, dtype=torch.uint8), workspace_bytes=9)):
+        refused(api.MX_ERR_SHAPE, run, **bad)
+    refused(api.MX_ERR_FORMAT, run, q=t(3, 4, 64, dtype=torch.bfloat16))
+    with pytest.raises(TypeError):
+        run()
