@@ -9,6 +9,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
@@ -27,6 +29,18 @@ struct Vec<_Float16> {
   // are scaled by 2^15 (which cancels in the division by their sum). bfloat16 has the range.
   static constexpr float kShift = 15.0f, kLeast = 0x1p-24f;
   static MX_DEV uint32_t cut(float a, float b) { return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b)); }
+  // Eight probabilities as both values. (What is left is cut too, 2^-22 of p at most; it is not negative, so its bits compare as integers.)
+  static MX_DEV void split(const float (&x)[8], x8& p, x8& rest) {
+    u32x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const auto both = __builtin_amdgcn_cvt_pkrtz(x[2 * i], x[2 * i + 1]);
+      hi[i] = __builtin_bit_cast(uint32_t, both);
+      const uint32_t left = cut(x[2 * i] - (float)both[0], x[2 * i + 1] - (float)both[1]);
+      lo[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(s16x2, left), (s16x2){1, 1}));
+    }
+    p = __builtin_bit_cast(x8, hi), rest = __builtin_bit_cast(x8, lo);
+  }
   static MX_DEV f32x4 mfma(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
   static MX_DEV f32x16 mfma(x8 a, x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
   template <bool HI>
@@ -39,6 +53,18 @@ struct Vec<__bf16> {
   typedef bf16x8 x8;
   static constexpr float kShift = 0.0f, kLeast = 0x1p-126f;
   static MX_DEV uint32_t cut(float a, float b) { return __builtin_amdgcn_perm(fbits(b), fbits(a), 0x07060302u); }
+  static MX_DEV void split(const float (&x)[8], x8& p, x8& rest) {
+    u32x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      hi[i] = cut(x[2 * i], x[2 * i + 1]);
+      bf16x2 left;
+#pragma unroll
+      for (int e = 0; e < 2; e++) left[e] = (__bf16)(x[2 * i + e] - bitsf(fbits(x[2 * i + e]) & 0xFFFF0000u));
+      lo[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(s16x2, left), (s16x2){0x80, 0x80}));
+    }
+    p = __builtin_bit_cast(x8, hi), rest = __builtin_bit_cast(x8, lo);
+  }
   static MX_DEV f32x4 mfma(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
   static MX_DEV f32x16 mfma(x8 a, x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
   template <bool HI>
@@ -67,12 +93,13 @@ MX_DEV float soft_cap(float s, float c) {
   return fabsf(y) < 0.2f ? near : far;
 }
 
-// Partial results of positions that rows share, for the kernel that goes on with each row's own. A slot holds 32 query rows: the outputs
-// [dim / 4][32] quads, then [32] {maximum, sum}, as the kernels hold them. rows[b] of sequence b: first slot of its group, slots of 32 rows, slots of a
-// head's 32 rows / of a group's head / the sequence's first row in its group.
-constexpr int kPrefixRows = 32;
+// Partial results of positions that rows share, for the kernel that goes on with each row's own. A unit is 128 query rows of a group and
+// cache head, in four slots of 32 for each of the splits of its keys, which are next to each other: the outputs [dim / 4][32] quads, then [32] {maximum,
+// sum}, as the kernels hold them.
+constexpr int kPrefixRows = 32, kPrefixSlots = 4, kPrefixUnit = kPrefixRows * kPrefixSlots;
 struct Prefix {
-  const i32x4* rows;      // {first slot, splits (0: none), tiles of 32 rows, first row}
+  const i32x4* rows;      // of sequence b: {its group's first unit, units of a cache head, first row in its group, whether it shares}
+  const int2* units;      // {first split, splits}
   const float* partial;   // NULL: no shared positions
 };
 MX_HD int64_t prefix_slot_floats(int dim) { return (int64_t)kPrefixRows * (dim + 2); }

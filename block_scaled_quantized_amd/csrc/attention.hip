@@ -618,6 +618,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
       }
     }
 
+    // On its way during the merge: where the results of the positions that the row shares are.
+    i32x4 shared_at = {0, 0, 0, 0};
+    if (fresh(args)->prefix.partial) shared_at = fresh(args)->prefix.rows[b];
+
     // Merge the waves, referred to their common maximum: half of them put their rows into LDS, the others add
     // theirs, and the readers below add the remaining ones.
 #pragma unroll
@@ -671,32 +675,33 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
     const auto put_lse = [&](int h, float top, float sum) {
       if (z.lse) z.lse[(int64_t)b * z.heads * z.group + first_head + h] = sum == 0.f ? -INFINITY : kLn2 * (top - kShift + __log2f(sum));
     };
-    // The head's results of the positions that its row shares, four splits of them at a time.
+    // The head's results of the positions that its row shares, kDeep splits of them at a time.
     const auto add_shared = [&](int h, int d, f32x4& o, float& top, float& sum) {
-      if (!z.prefix.partial) return;
-      const i32x4 r = z.prefix.rows[b];
-      const int splits = r[1], head = r[3] + kHeads * ht + h;
-      const int64_t size = prefix_slot_floats(dim);
-      const float* p = z.prefix.partial + (r[0] + (int64_t)(hk * r[2] + head / kPrefixRows) * splits) * size;
+      if (!shared_at[3]) return;
+      const int head = shared_at[2] + kHeads * ht + h;
+      const int2 unit = z.prefix.units[shared_at[0] + hk * shared_at[1] + head / kPrefixUnit];
+      const int splits = unit.y;
+      const int64_t slot = prefix_slot_floats(dim), size = kPrefixSlots * slot;
+      const float* p = z.prefix.partial + unit.x * size + head % kPrefixUnit / kPrefixRows * slot;
       const int outs = (d * (kPrefixRows / 4) + head % kPrefixRows) * 4, stats = kPrefixRows * dim + 2 * (head % kPrefixRows);
 #pragma unroll 1
-      for (int i = 0; i < splits; i += 4, p += 4 * size) {
-        float m[4], l[4];
-        f32x4 v[4];
+      for (int i = 0; i < splits; i += kDeep, p += kDeep * size) {
+        float2 w[kDeep];
+        f32x4 v[kDeep];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
+        for (int u = 0; u < kDeep; u++) {
           const int64_t at = i + u < splits ? u * size : 0;
-          m[u] = p[at + stats], l[u] = p[at + stats + 1], v[u] = *reinterpret_cast<const f32x4*>(p + at + outs);
+          w[u] = *reinterpret_cast<const float2*>(p + at + stats), v[u] = *reinterpret_cast<const f32x4*>(p + at + outs);
         }
-        float most = fmaxf(top, m[0]);
+        float most = fmaxf(top, w[0].x);
 #pragma unroll
-        for (int u = 1; u < 4; u++) most = fmaxf(most, m[u]);
+        for (int u = 1; u < kDeep; u++) most = fmaxf(most, w[u].x);
         const float ref = finite_or_zero(most), f = __builtin_amdgcn_exp2f(top - ref);
         o *= f, sum *= f, top = most;
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const float w = i + u < splits ? __builtin_amdgcn_exp2f(m[u] - ref) : 0.f;
-          if (w > 0.f) o += v[u] * w, sum += l[u] * w;
+        for (int u = 0; u < kDeep; u++) {
+          const float x = i + u < splits ? __builtin_amdgcn_exp2f(w[u].x - ref) : 0.f;
+          if (x > 0.f) o += v[u] * x, sum += w[u].y * x;
         }
       }
     };

@@ -9,6 +9,7 @@ from gpu_common import dev, require_gpu, say
 
 pytestmark = pytest.mark.gpu
 COUNTERS = 3 * 512 * 4
+FAR = 1 << 22   # bounds that are far above the lengths, for which the call shares whatever little there is
 
 
 class Batch:
@@ -44,9 +45,9 @@ class Batch:
     def run(self, softcap=0.0, max_len=None, max_shared=None, sharing=True, ws=None, shared=None):
         api = require_gpu()
         n, hq, dim = self.q.shape
-        max_len = max_len or max(1, int(self.lengths.max()))
+        max_len = max_len or FAR
         shared = self.shared if shared is None else np.array(shared, np.int32)
-        most = int(max(1, shared.max())) if max_shared is None else max_shared
+        most = FAR if max_shared is None else max_shared
         need = api.mxattn_prefix_workspace_size(self.c.c, n, hq, len(shared), max_len, most)
         if ws is None:
             ws = torch.full((max(16, need),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN wherever nothing is written
@@ -155,9 +156,9 @@ def test_bounds():
     b = Batch("f16", "f16", "heads", 128, 16, 2, 4, [4], [600], 40)
     for most in (1, 64, 100, 1 << 20):
         b.check(*b.run(max_shared=most))
-    b.check(*b.run(max_len=100000))
-    b.check(*b.run(shared=[1 << 30], max_shared=600))
-    b.check(*b.run(shared=[-7], max_shared=600))
+    b.check(*b.run(max_len=int(b.lengths.max()), max_shared=600))
+    b.check(*b.run(shared=[1 << 30]))
+    b.check(*b.run(shared=[-7]))
     full = b.lengths.copy()
     out, lse = b.run(max_len=500)
     b.lengths = np.minimum(full, 500)
@@ -169,6 +170,14 @@ def test_falling_firsts_share_nothing():
     for first in ([0, 5, 2], [4, 0, 5], [-9, 99, 3]):
         b.first = np.array(first, np.int32)
         b.check(*b.run())
+
+
+def test_little_to_share():
+    """Where the bounds leave less to share than a pass of its own costs, every row is read by itself."""
+    b = Batch("f16", "f16", "heads", 128, 16, 2, 4, [4, 3], [600, 300], 40)
+    api, n, hq = require_gpu(), *b.q.shape[:2]
+    assert api.mxattn_prefix_workspace_size(b.c.c, n, hq, 2, 700, 600) == api.mxattn_decode_workspace_size(b.c.c, n, hq, 700)
+    b.check(*b.run(max_len=700, max_shared=600))
 
 
 def test_without_workspace():
@@ -212,12 +221,12 @@ def test_strides_and_streams():
     n, hq, dim = b.q.shape
     out_wide = torch.full((4, 9, 72), float("nan"), dtype=torch.float16, device="cuda")
     out, lse = out_wide[:, 1:7, :64], torch.zeros(n, hq, device="cuda")
-    need = api.mxattn_prefix_workspace_size(b.c.c, n, hq, 1, 400, 300)
+    need = api.mxattn_prefix_workspace_size(b.c.c, n, hq, 1, FAR, FAR)
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
     args = [dev(t) for t in (b.table, b.lengths, b.first, b.shared)]
     stream = torch.cuda.Stream()
     torch.cuda.synchronize()
-    api.mxattn_prefix_run(b.c.c, api.MX_F16, b.q, out, args[0], args[1], 400, args[2], args[3], 300, dim ** -0.5, lse=lse, workspace=ws, stream=stream)
+    api.mxattn_prefix_run(b.c.c, api.MX_F16, b.q, out, args[0], args[1], FAR, args[2], args[3], FAR, dim ** -0.5, lse=lse, workspace=ws, stream=stream)
     stream.synchronize()
     b.check(out, lse)
     assert int(out_wide.isnan().sum()) == out_wide.numel() - out.numel()
@@ -229,11 +238,11 @@ def test_graph():
     b = Batch("f16", "f16", "heads", 128, 16, 2, 4, [4, 3], [600, 300], 200)
     n, hq, dim = b.q.shape
     out, lse = torch.zeros_like(b.q), torch.zeros(n, hq, device="cuda")
-    ws = torch.zeros(api.mxattn_prefix_workspace_size(b.c.c, n, hq, 2, 1000, 700), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(api.mxattn_prefix_workspace_size(b.c.c, n, hq, 2, FAR, FAR), dtype=torch.uint8, device="cuda")
     table, lengths, first, shared = (dev(t) for t in (b.table, b.lengths, b.first, b.shared))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        api.mxattn_prefix_run(b.c.c, api.MX_F16, b.q, out, table, lengths, 1000, first, shared, 700, dim ** -0.5, lse=lse, workspace=ws)
+        api.mxattn_prefix_run(b.c.c, api.MX_F16, b.q, out, table, lengths, FAR, first, shared, FAR, dim ** -0.5, lse=lse, workspace=ws)
     full = b.lengths.copy()
     for i, (new_shared, cut) in enumerate((([600, 300], 0), ([0, 128], 3), ([592, 64], 50), ([600, 300], 0))):
         b.lengths = np.maximum(full - cut, 0).astype(np.int32)
@@ -251,3 +260,11 @@ def test_deterministic():
     first = b.run()
     for _ in range(3):
         assert all(torch.equal(x, y) for x, y in zip(first, b.run()))
+
+
+@pytest.mark.parametrize("kind,cache,dim,heads", [("f16", "f16", 40, 12), ("bf16", "e4m3", 64, 12), ("bf16", "bf16", 72, 12), ("f16", "e4m3", 96, 12), ("f16", "f16", 136, 6),
+                                                  ("bf16", "e4m3", 160, 6)])
+def test_many_tiles(kind, cache, dim, heads):
+    """Workgroups with more tiles than they look up the pages of at a time, which end one unit and begin another."""
+    b = Batch(kind, cache, "heads", dim, 16, heads, 1, [2], [20000], 20)
+    b.check(*b.run())

@@ -195,9 +195,10 @@ def test_prefix_refusals(status, args):
 def test_prefix_workspace_sizes():
     size, c = api.mxattn_prefix_workspace_size, cache_of()
     assert size(c, 0, 4, 2, 100, 100) == size(c, 3, 3, 2, 100, 100) == size(c, 3, 4, -1, 100, 100) == size(c, 3, 4, 1025, 100, 100) == size(c, 3, 4, 2, 100, -1) == 0
-    for args in ((1, 4, 1, 5000, 5000), (9, 4, 0, 5000, 5000), (9, 4, 2, 5000, 63), (9, 4, 2, 63, 5000)):  # nothing to share
+    # nothing to share, or too little
+    for args in ((1, 4, 1, 50000, 50000), (9, 4, 0, 50000, 50000), (9, 4, 9, 50000, 50000), (9, 4, 2, 50000, 63), (9, 4, 2, 63, 50000), (9, 4, 2, 50000, 2000)):
         assert size(c, *args) == api.mxattn_decode_workspace_size(c, *args[:2], args[3])
-    assert size(c, 9, 4, 2, 5000, 64) > api.mxattn_decode_workspace_size(c, 9, 4, 5000)
+    assert size(c, 9, 4, 2, 50000, 40000) > api.mxattn_decode_workspace_size(c, 9, 4, 50000)
     with pytest.raises(api.MXError):
         size(c, 9, 4, 2, 1 << 40, 64)
 
