@@ -9,6 +9,11 @@
 //
 // The shared positions of a group end where the shortest of its rows does, and with a whole tile: what is left is the rows' own, so
 // no key here is masked for some rows and not for others.
+//
+// What bounds it: one round of workgroups, each of which works out the shares and fetches its first keys (some 15000 clocks) before turns of 128
+// keys, 6100 to 6700 clocks for 128 rows, in which the matrix cores have 35% and the vector units most of the rest. 64 rows of 64 heads behind 8192
+// positions of 8 x 128 bf16: 38 us here, 36 in the decode kernel (512 positions of each row and the joining of 17 MB of partial results), where
+// the decode kernel alone would read 2.2 GB. 96 rows in five groups behind up to 12000 positions, E4M3: 80 to 95 us and 52.
 #include <algorithm>
 
 #include "attention.h"

@@ -4,7 +4,8 @@
 // Integers throughout. Rows' pages and tokens are counted, summed over the rows before each (one workgroup, a row per thread), and
 // the pages and tokens then numbered through: thread i finds the row of page or token i by bisection of the sums. The free pages are
 // a stack; what a call gives back goes onto it in the order that undoes taking the same pages. Bound by the chain of dependent
-// memory latencies (rows, stack, table, slots), so one launch does all where the tokens are few.
+// memory latencies (rows, stack, table, slots), so one launch does all where the tokens are few: 256 rows, one token each, 4.6 us, of which a kernel
+// of one store takes 3.6. With more tokens than one workgroup writes in the time of a launch, a second kernel writes them.
 #include <algorithm>
 
 #include "kvcache.h"

@@ -499,8 +499,9 @@ typedef struct {
  *  - There is no window (opts->window: 0) and there are no starts. Other rules, and the treatment of missing pages, empty rows and lse, are
  *    mxattn_decode_run's; 0 <= count <= 1024, max_shared >= 0 (MX_ERR_SHAPE).
  *  - Results are the same up to fp32 summation order.
- * Workspace as for mxattn_decode_run, of mxattn_prefix_workspace_size() bytes (the buffers of the two are interchangeable where large enough). Without one, or with too small a one,
- * nothing is shared: every row is read by itself.
+ * Workspace as for mxattn_decode_run, of mxattn_prefix_workspace_size() bytes (the buffers of the two are interchangeable where large enough). Without
+ * one, or with too small a one, nothing is shared: every row is read by itself. So it is where max_len, max_shared and the numbers of rows and groups leave less
+ * than some 64 MB that need not be read again, as a pass of its own would take longer; the results are those of mxattn_decode_run then.
  */
 int mxattn_prefix_run(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, float* lse, const mxkv_table* table,
                       const int32_t* lengths, const mxattn_groups* groups, int max_len, const mxattn_opts* opts, void* workspace,
