@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(Args a, int fill) {
     Sums x, more;
     scan(row_of(a, b0 + t), x, more, waves);
 #pragma unroll
-    for (int i = 0; i < kKinds; i++) all.n[i] = cut(all.n[i] + more.n[i]);
+    for (int i = 0; i < kKinds; i++) all.n[i] = cut(cut(all.n[i]) + more.n[i]);
   }
   const int top = n_free + all.n[kGives];  // of the stack, when everything is given back
   const int status = (all.n[kBad] ? MXKV_STEP_LONG : 0) | (all.n[kTokens] > a.max_tokens ? MXKV_STEP_TOKENS : 0) |

@@ -102,6 +102,22 @@ def test_refusals_on_the_device(seqs):
     assert s.call([s.lengths[0]] + [-1] * (seqs - 1)) == 0
 
 
+@pytest.mark.parametrize("seqs", [1024, 1025, 2100, 3000])
+def test_sums_past_32_bits(seqs):
+    """Rows that together want more tokens and pages than 32 bits count: refused, and nothing changes."""
+    api = require_gpu()
+    page, cols, pages = 2, 540000, 7
+    full = lambda n, v: torch.full((n,), v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.full((seqs, cols), -1, dtype=torch.int32, device="cuda")
+    lengths, free, n_free, status, offsets = full(seqs, 0), torch.arange(pages, dtype=torch.int32, device="cuda"), full(1, pages), full(1, 77), full(seqs + 1, 77)
+    maps = [full(16, 77) for _ in range(3)]
+    say(f"{seqs} rows that want all of {cols} pages")
+    api.mxkv_step_run(page, table, lengths, full(seqs, page * cols), free, n_free, offsets, *maps, status)
+    torch.cuda.synchronize()
+    assert status.item() == api.MXKV_STEP_PAGES | api.MXKV_STEP_TOKENS
+    assert not lengths.any() and n_free.item() == pages and not offsets.any() and bool((table == -1).all()) and all(bool((m == -1).all()) for m in maps)
+
+
 def test_stack_that_is_not_free():
     """A stack that says it is full while rows hold pages is not written past its end."""
     s = Step(2, 4, 2, 8, 16, 1)
