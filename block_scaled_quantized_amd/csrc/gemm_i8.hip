@@ -54,7 +54,7 @@ MX_DEV uint32_t extent(int rows, int64_t ld, int K) { return (uint32_t)((rows - 
 
 template <typename T>
 MX_DEV T finished(int sum, float scale, float bias, bool relu) {
-  float v = (float)sum * scale + bias;
+  float v = fmaf((float)sum, scale, bias);
   if (relu) v = fmaxf(v, 0.f);
   return (T)v;
 }
