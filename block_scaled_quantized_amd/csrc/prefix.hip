@@ -13,7 +13,7 @@
 // What bounds it: one round of workgroups, each of which works out the shares and fetches its first keys (some 15000 clocks) before turns of 128
 // keys, 6100 to 6700 clocks for 128 rows, in which the matrix cores have 35% and the vector units most of the rest. 64 rows of 64 heads behind 8192
 // positions of 8 x 128 bf16: 38 us here, 36 in the decode kernel (512 positions of each row and the joining of 17 MB of partial results), where
-// the decode kernel alone would read 2.2 GB. 96 rows in five groups behind up to 12000 positions, E4M3: 80 to 95 us and 52.
+// the decode kernel alone takes 335. 96 rows in five groups behind up to 12000 positions, E4M3: 80 to 95 us and 52, alone 232.
 #include <algorithm>
 
 #include "attention.h"
@@ -56,7 +56,7 @@ struct Plan {
   int* work;     // [groups + 1] tiles before the group's
   int* units;    // units before the group's
   int* end;      // shared positions
-  int* members;  // with positions
+  int* lead;     // first sequence with positions, whose table row names the shared pages
 };
 constexpr int plan_ints(int groups) { return 5 * (groups + 1); }
 MX_DEV Plan plan_in(int* lds, int groups) {
@@ -119,16 +119,16 @@ MX_DEV Shares plan(const Args& a, const Plan& p, int tile) {
   for (int g = t; g <= a.groups; g += THREADS) {
     const int f = a.first[g], n = a.shared[min(g, a.groups - 1)];
     p.first[g] = max(0, min(f, a.seqs));
-    p.end[g] = max(0, min(n, a.max_shared)), p.members[g] = 0;
+    p.end[g] = max(0, min(n, a.max_shared)), p.lead[g] = a.seqs, p.work[g] = 0;
   }
   if (t == 0) all_work = 0, falls = 0;
   __syncthreads();
   for (int g = t; g < a.groups; g += THREADS)
     if (p.first[g + 1] < p.first[g]) falls = 1;
-  // rows without positions do not count; a beginning that no two rows share is not worth its own pass
+  // rows without positions do not count (work: the others, for now); a beginning that no two rows share is not worth its own pass
   for (int b = t; b < a.seqs; b += THREADS) {
     const int n = length_of(a, b == t ? own : a.lengths[b]), g = group_of(p, a.groups, b);
-    if (g >= 0 && n > 0) atomicMin(&p.end[g], n), atomicAdd(&p.members[g], 1);
+    if (g >= 0 && n > 0) atomicMin(&p.end[g], n), atomicMin(&p.lead[g], b), atomicAdd(&p.work[g], 1);
   }
   __syncthreads();
   int work[kOfThread], units[kOfThread], my_work = 0, my_units = 0;
@@ -137,7 +137,7 @@ MX_DEV Shares plan(const Args& a, const Plan& p, int tile) {
     const int g = t * kOfThread + i;
     work[i] = my_work, units[i] = my_units;
     if (g >= a.groups) continue;
-    p.end[g] = p.members[g] < 2 || falls || p.end[g] < kLeastShared ? 0 : p.end[g] & ~(kGrain - 1);
+    p.end[g] = p.work[g] < 2 || falls || p.end[g] < kLeastShared ? 0 : p.end[g] & ~(kGrain - 1);
     const Shape s = shape_of(a, p, g, tile);
     mine += (unsigned long long)a.heads * s.tiles * s.keys;
     my_work += a.heads * s.tiles * s.keys, my_units += a.heads * s.tiles;
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(threads_of(D), halves_of(D)) void prefix_kernel(Arg
     x += end - begin;
     const int64_t slot = ((int64_t)(share + unit) * kRowWaves + row_wave) * prefix_slot_floats(dim);
     const int64_t head_at = (int64_t)hk * a.head_stride;
-    const int32_t* table = a.table + (int64_t)first * a.cols;
+    const int32_t* table = a.table + (int64_t)uniform(groups.lead[g]) * a.cols;
     const int row0 = row_tile * kRows + 32 * row_wave;
 
     // The keys of tiles begin + kBlock b and on, one to a thread: its page, then its place.

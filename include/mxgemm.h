@@ -328,8 +328,8 @@ int mxquant_rows_run(int f, int rows, int dim, const mx_rows* x, int fmt, const 
  * row of A (token) and one per row of B (output channel).
  *   A int8 [M][K], SA fp32 [M]; B int8 [N][K] (K contiguous, as the block-scaled GEMM's), SB fp32 [N]; C [M][N] in fc, MX_F16, MX_BF16 or
  *   MX_F32; bias [N] in fc (NULL: none); flags: 0 or MXGEMM_RELU (C = max(C, 0), after the bias).
- * The sum is exact; it, the scales' product and theirs are rounded to fp32, the bias is added, and the result is
- * rounded to fc. Results are the same bits for every workspace.
+ * The sum is exact; it and the scales' product are rounded to fp32, their product with the bias added once more, and the result is
+ * rounded to fc (ReLU makes NaN 0, as mxgemm_run's). Results are the same bits for every workspace.
  * 0 <= M <= MX_MAX_DIM (0: nothing is done), 1 <= N <= MX_MAX_DIM, 1 <= K <= MXGEMM_I8_MAX_K, all odd ones among them. Strides: A's and B's at least K and
  * multiples of 16, at most MX_MAX_DIM; C's at least N (rows of C that are not 16-byte aligned are written by
  * elements). Every row of A and B, the last one too, is read up to the next multiple of 16 bytes past K; what stands there does
@@ -492,7 +492,7 @@ typedef struct {
 
 /*
  * mxattn_prefix_run -- mxattn_decode_run for a batch whose rows share long beginnings: the same results, but a group's shared keys
- * and values are read once for all of its rows, through the table row of its first sequence. Each row's table still names all of
+ * and values are read once for all of its rows, through the table row of its first sequence that has positions. Each row's table still names all of
  * its pages, as after mxkv_pool_fork; lengths count all positions, the shared ones among them.
  *  - What is shared is cut to the group's shortest row that has positions, and to whole tiles of 64; a row's other positions are read through
  *    its own table row. A group with one row that has positions shares nothing.

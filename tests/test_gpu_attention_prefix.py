@@ -123,6 +123,15 @@ def test_shared_through_the_first_row():
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+def test_rows_that_have_ended(cache):
+    """A group goes on when its first rows end: rows without positions, whose tables name no pages, do not count."""
+    b = Batch("f16", cache, "heads", 128, 16, 2, 4, [4, 3, 2], [512, 320, 256], 40, outside=(1, 1))
+    for row in (1, 2, 5, 8):
+        b.lengths[row], b.table[row] = 0, -1
+    b.check(*b.run())
+
+
 def test_missing_pages():
     """Positions whose page is missing are left out, in what is shared too; a whole group may have none."""
     b = Batch("f16", "f16", "heads", 128, 16, 2, 4, [3, 2], [512, 256], 40)
