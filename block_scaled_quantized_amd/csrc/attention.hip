@@ -700,8 +700,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
         o *= f, sum *= f, top = most;
 #pragma unroll
         for (int u = 0; u < kDeep; u++) {
-          const float x = i + u < splits ? __builtin_amdgcn_exp2f(w[u].x - ref) : 0.f;
-          if (x > 0.f) o += v[u] * x, sum += w[u].y * x;
+          const float x = __builtin_amdgcn_exp2f(w[u].x - ref);  // NaN where the maximum is infinite
+          // (a part that counts nothing is left out, unless it is NaN)
+          if (i + u < splits && (x != 0.f || w[u].y != w[u].y)) o += v[u] * x, sum += w[u].y * x;
         }
       }
     };

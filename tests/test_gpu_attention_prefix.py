@@ -209,6 +209,21 @@ def test_one_workspace_for_all():
             b.check(out, lse)
 
 
+def test_infinite_scores_and_nan_queries():
+    """NaN where the rows by themselves give it: queries with NaN, of rows that share all they have too, and scores that are infinite, which softmax
+    makes NaN (a score of -infinity counts nothing)."""
+    b = Batch("f16", "f16", "heads", 128, 16, 2, 4, [3, 2], [320, 256], [0, 30, 0, 20, 0])
+    b.q[0, 3, 7] = b.q[1, 5, 0] = float("nan")
+    b.c.planes[0][int(b.table[3, 2]), 1, 3, 9] = float("inf")
+    b.q[3, 4, 9], b.q[3, 5, 9], b.q[4, 4, 9], b.q[4, 5, 9] = 1.0, -1.0, -1.0, 1.0
+    (out, lse), (want, want_lse) = b.run(), b.run(sharing=False)
+    for row, head, bad in ((0, 3, True), (1, 5, True), (2, 5, False), (3, 4, True), (3, 5, False), (4, 4, False), (4, 5, True)):
+        assert bool(want[row, head].isnan().all()) == bool(want[row, head].isnan().any()) == bad
+    assert torch.equal(out.isnan(), want.isnan()) and torch.equal(lse.isnan(), want_lse.isnan())
+    # two results off by half a step of binary16, and by what the sums lose, each
+    assert ((out - want).abs().nan_to_num() <= 4 * 2.0 ** -11 * want.abs().nan_to_num().max()).all()
+
+
 def test_infinite_values_and_nan():
     """A shared value that is infinite or NaN reaches every row of the group and no other row."""
     for bad in (float("inf"), float("nan")):
