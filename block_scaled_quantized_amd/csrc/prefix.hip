@@ -615,8 +615,8 @@ bool sizes_ok(int groups, int max_shared) { return groups >= 0 && groups <= kMax
 // Whether there may be enough to share: a pass of its own and the joining of its results take some 12 us, in which the decode kernel reads 64 MB
 // (4 rows behind 992 positions of 8 x 128 fp16, 12 MB that need not be read again: 11.5 us without, 20 with).
 bool worth(const mxkv_cache* c, int seqs, int groups, int max_len, int max_shared) {
-  const int64_t shared = std::min(max_len, max_shared), again = std::max(0, seqs - groups);
-  return groups > 0 && shared >= kLeastShared && again * shared * c->heads * c->dim * (c->fmt == MX_E4M3 ? 2 : 4) >= (int64_t)64 << 20;
+  const int shared = std::min(max_len, max_shared), again = std::max(0, seqs - groups);
+  return groups > 0 && shared >= kLeastShared && (double)again * shared * c->heads * c->dim * (c->fmt == MX_E4M3 ? 2 : 4) >= (double)(64 << 20);
 }
 
 Space space_for(const mxkv_cache* c, int seqs, int q_heads, int groups, int max_len) {

@@ -160,6 +160,13 @@ def test_many_groups():
     b.check(*b.run())
 
 
+@pytest.mark.parametrize("cache,dim", [("e4m3", 128), ("f16", 256)])
+def test_most_groups(cache, dim):
+    """As many groups as there may be, whose lists need the most LDS; some have one row, or none."""
+    b = Batch("f16", cache, "heads", dim, 16, 1, 1, [i % 4 for i in range(1024)], [64 + 64 * (i % 2) for i in range(1024)], 9)
+    b.check(*b.run())
+
+
 def test_bounds():
     """shared above max_shared is taken as it, lengths above max_len too; bounds far above both change nothing."""
     b = Batch("f16", "f16", "heads", 128, 16, 2, 4, [4], [600], 40)
