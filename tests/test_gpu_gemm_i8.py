@@ -74,6 +74,13 @@ def test_large_tiles(M, N, K):
     run(M, N, K, "f16", 1)
 
 
+@pytest.mark.parametrize("K", [1, 16, 128, 129, 257, 400, 513, 1157])
+@pytest.mark.parametrize("M,N,kind", [(1500, 2100, "f16"), (1000, 3201, "f32"), (2200, 3001, "bf16"), (1800, 3500, "f32"), (3500, 3701, "f16"), (3300, 3800, "f32")])
+def test_rings(M, N, kind, K):
+    """One to ten slots of K through the rings of tiles 128 wide, for as many workgroups as there are CUs and for more, and 256 wide."""
+    run(M, N, K, kind, K, pad=(K % 2, K % 3), bias=bool(K % 2), relu=bool(K % 3))
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(3, 70, 200), (100, 200, 1500), (2100, 6200, 160)])
 def test_types_bias_relu(kind, M, N, K):
