@@ -38,6 +38,7 @@ struct Args {
   int64_t x_stride, residual_stride, total_stride, out_stride;  // elements
   int rows, dim;
   float eps, inv_dim;
+  double inv;  // 1 / dim
   int norm;
 };
 
@@ -57,6 +58,10 @@ MX_DEV uint32_t add_bits(uint32_t a, uint32_t b) { return fbits(bitsf(a) + bitsf
 MX_DEV uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }  // of magnitudes: NaN above infinity above all
 MX_DEV uint32_t magnitude(float x) { return fbits(x) & 0x7FFFFFFFu; }
 constexpr uint32_t kInf = 0x7F800000u;
+MX_DEV uint32_t quad_max(uint32_t x) {  // over four neighbouring lanes
+  x = max_bits(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false));  // quad_perm: 1 away, 2 away
+  return max_bits(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false));
+}
 
 // The exponent e of a positive finite number, 2^e <= x (subnormal ones count as -127), and 2^-e in two factors.
 MX_DEV int exponent_of(uint32_t bits) { return max(-126, (int)(bits >> 23) - 127); }
@@ -124,18 +129,21 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
       }
     }
   };
-  // the row's sum of squares and largest magnitude, from the threads' own
+  // the row's sum of squares and largest magnitude, from the threads' own (the waves' sums are added in 64 bits)
+  double whole_sum = 0.0;
   const auto reduce = [&](float& sum, uint32_t& top) {
     uint32_t s = wave_all(fbits(sum), add_bits);
     top = wave_all(top, max_bits);
     if constexpr (W > 1) {
       if ((threadIdx.x & 63) == 0) wave_sum[wave] = s, wave_top[wave] = top;
       __syncthreads();
-      s = wave_sum[0], top = wave_top[0];
+      whole_sum = (double)bitsf(wave_sum[0]), top = wave_top[0];
 #pragma unroll
-      for (int w = 1; w < W; w++) s = add_bits(s, wave_sum[w]), top = max_bits(top, wave_top[w]);
+      for (int w = 1; w < W; w++) whole_sum += (double)bitsf(wave_sum[w]), top = max_bits(top, wave_top[w]);
+      sum = (float)whole_sum;
+    } else {
+      sum = bitsf(s), whole_sum = (double)sum;
     }
-    sum = bitsf(s);
   };
 
   float sum = 0.f;
@@ -165,7 +173,8 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
 #pragma unroll
     for (int u = 0; u < U; u++) count(wide(held[u]), c + t + u * kLanes);
   }
-  float factor = 1.f, pre = 1.f, pre2 = 1.f;  // y = (h pre pre2 w) factor
+  constexpr bool kBlocks = OUT == MX_E4M3 || OUT == MX_E5M2;
+  float factor = 1.f, low = 0.f, pre = 1.f, pre2 = 1.f;  // y = (h pre pre2 w) (factor + low), low: what the factor's rounding leaves, for blocks
   if (a.norm || OUT == MX_INT8) reduce(sum, top);
   if (a.norm) {
     float eps = a.eps;
@@ -195,6 +204,12 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
       }
     }
     factor = __builtin_amdgcn_rsqf(fmaf(sum, a.inv_dim, eps));
+    if (kBlocks && factor > 0.f && factor < INFINITY) {
+      // A block's scale jumps where its largest element passes a power of two, so that element counts to its last bit: one step of Newton's
+      // in 64 bits from the approximation.
+      const double f = (double)factor, v = whole_sum * a.inv + (double)eps, r = f * (1.5 - 0.5 * v * f * f);
+      factor = (float)r, low = (float)(r - (double)factor);
+    }
   }
 
   const auto g_of = [&](x8 v, int i) -> f32x8 {
@@ -228,12 +243,31 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
     uint8_t* out = (uint8_t*)a.out + row * a.out_stride;
     uint8_t* scales = (uint8_t*)a.scales + (int64_t)row * (dim / 32);
     each([&](int i, x8 v) {
-      f32x8 y = g_of(v, i) * factor;
+      const f32x8 g = g_of(v, i);
+      f32x8 y, rest = g * low;
+      if constexpr (sizeof(T) == 4) {  // 16-bit elements' products with the weights are exact
+        if (weight) {
+          f32x8 h = wide(v);
+          if (pre != 1.f || pre2 != 1.f) h = h * pre * pre2;
+          const f32x8 w = wide(load(weight, i));
+#pragma unroll
+          for (int e = 0; e < 8; e++) rest[e] = fmaf(fmaf(h[e], w[e], -g[e]), factor, rest[e]);
+        }
+      }
       uint32_t amax = 0u;
 #pragma unroll
-      for (int e = 0; e < 8; e++) amax = max_bits(amax, magnitude(y[e]));
-      amax = max_bits(amax, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)amax, 0xB1, 0xF, 0xF, false));  // quad_perm: the lane's
-      amax = max_bits(amax, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)amax, 0x4E, 0xF, 0xF, false));  // neighbours 1 and 2 away
+      for (int e = 0; e < 8; e++) y[e] = fmaf(g[e], factor, rest[e]), amax = max_bits(amax, magnitude(y[e]));
+      amax = quad_max(amax);
+      if (__any((amax & 0x7FFFFFu) == 0u && amax > 0u && amax < kInf)) {  // a power of two, or what was rounded up to it
+        uint32_t below = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float left = fmaf(g[e], factor, -y[e]) + rest[e];  // of y's rounding
+          below = max_bits(below, magnitude(y[e]) - ((left < 0.f && y[e] > 0.f) || (left > 0.f && y[e] < 0.f) ? 1u : 0u));
+        }
+        below = quad_max(below);
+        if (amax < kInf) amax = below;
+      }
       int shift;
       const uint32_t E = mx_block_scale(amax, amax >= kInf, OUT, &shift);
       if (i >= units) return;
@@ -327,7 +361,7 @@ int run(Args a, int f, int rows, int dim, const mx_rows* x, const mx_rows* resid
   if (residual) a.residual = residual->data, a.residual_stride = residual->stride;
   if (total) a.total = total->data, a.total_stride = total->stride;
   a.out = out->data, a.out_stride = out->stride, a.scales = scales;
-  a.inv_dim = (float)(1.0 / dim);
+  a.inv = 1.0 / dim, a.inv_dim = (float)a.inv;
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
   if (f == MX_F16) launch_out<_Float16, MX_F16>(a, fmt, st);

@@ -99,6 +99,23 @@ def test_norm_blocks(fmt, bits, top, most, least, kind, rows, dim):
     assert err <= 1.0
 
 
+@pytest.mark.parametrize("fmt,top", [("MX_E4M3", 8), ("MX_E5M2", 15)])
+@pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,dim", [(1, 64), (1030, 96), (3, 4096), (1100, 2048), (2, 8192), (2, 40000)])
+def test_scales_at_powers_of_two(fmt, top, kind, rows, dim):
+    """A block's scale is that of y before its rounding: elements +-c of one size have y = c / sqrt(c^2 + eps), which is below 1 by less than fp32 holds with a small
+    eps, and 1 without one."""
+    api = require_gpu()
+    x = torch.where(torch.arange(rows * dim, device="cuda").reshape(rows, dim) % 3 == 0, -2.0, 2.0).to({"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[kind])
+    codes, scales = torch.zeros(rows, dim, dtype=torch.uint8, device="cuda"), torch.zeros(rows, dim // 32, dtype=torch.uint8, device="cuda")
+    for eps, e in ((1e-9, -1), (0.0, 0)):
+        api.mxnorm_run(fmt_of(api, kind), x, codes, scales, getattr(api, fmt), eps=eps)
+        assert bool((scales == 127 + e - top).all())
+        y = codes.view(torch.float8_e4m3fn if fmt == "MX_E4M3" else torch.float8_e5m2).float() * 2.0 ** (e - top)
+        # scaled to 2^(top + 1) less a little, which is cut to the largest element, 1.75 * 2^top
+        assert torch.equal(y, x.float() * (0.5 if e == 0 else 0.4375))
+
+
 def awkward(dim):
     """Rows of zeros, subnormals, one element, the largest values, infinities and NaN."""
     g = np.random.Generator(np.random.PCG64(9))
