@@ -383,13 +383,14 @@ __global__ __launch_bounds__(threads_of(D), halves_of(D)) void prefix_kernel(Arg
 #pragma unroll
           for (int e = 0; e < 16; e++) s[u][e] = soft_cap(s[u][e] * fabsf(a.scale), a.softcap);
       }
-      if (mask != ~0ull) {
+      float by = f;
+      if (mask != ~0ull) {  // scaled first: a scale of 0 times a masked score would be NaN
+        by = 1.f;
 #pragma unroll
         for (int u = 0; u < 2; u++) {
           const uint32_t mine = (uint32_t)(mask >> 32 * u) >> 4 * h;
 #pragma unroll
-          for (int e = 0; e < 16; e++)
-            if (!(mine >> (8 * (e / 4) + e % 4) & 1u)) s[u][e] = -INFINITY;
+          for (int e = 0; e < 16; e++) s[u][e] = mine >> (8 * (e / 4) + e % 4) & 1u ? s[u][e] * f : -INFINITY;
         }
       }
       float top = s[0][0];
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(threads_of(D), halves_of(D)) void prefix_kernel(Arg
       for (int u = 0; u < 2; u++)
 #pragma unroll
         for (int e = 0; e < 16; e++) top = fmaxf(top, s[u][e]);
-      top *= f;
+      top *= by;
       if (__any(top > m + kSlack)) {
         const auto r = __builtin_amdgcn_permlane32_swap(fbits(top), fbits(top), false, false);
         top = fmaxf(fmaxf(bitsf(r[0]), bitsf(r[1])), m);
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(threads_of(D), halves_of(D)) void prefix_kernel(Arg
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          x[e] = __builtin_amdgcn_exp2f(fmaf(s[st / 2][8 * (st % 2) + e], f, ref));
+          x[e] = __builtin_amdgcn_exp2f(fmaf(s[st / 2][8 * (st % 2) + e], by, ref));
           l += x[e];
         }
         Vec<T>::split(x, p[st], rest[st]);
