@@ -34,7 +34,6 @@ using namespace mx;
 
 namespace {
 
-
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kTile = 32;                // keys of a wave's tile
 constexpr int kGrain = kTile * kWaves;   // keys that the workgroup's waves take in turn: the unit of work
@@ -241,7 +240,8 @@ constexpr int tiles_ahead(int D, bool split, int ht = 1) { return D == 256 || ht
 constexpr bool query_in_lds(int D, int ht) { return D == 256 || ht > 1; }
 // Shares of D = 256 16-bit rows take more than 256 registers (16 x 8192 x 4 fp16: 88 us, spilled into 256 of them
 // 101; E4M3 fits: 64 us against 69), which whole units, small and many, do better without (200 x 4 rows of 30 keys:
-// 15 us against 25). Shares of D = 64 fit three waves (78 x 16 short rows E4M3: 17 us, 20 with two, 24 spilled into four).
+// 15 us against 25). Shares of D = 64 fit three waves (78 x 16 short rows E4M3: 17 us, 20 with two, 24 spilled into four), but for 7 to 9
+// registers of rows that go on from shared positions.
 constexpr int waves_per_simd(int D, bool mx8, bool split, int ht) { return !split || ht > 1 ? 2 : D == 64 ? 3 : D == 256 && !mx8 ? 1 : 2; }
 
 // D: 64, 128 or 256, the head size rounded up. T: type of q, out and the arithmetic. MX8: E4M3 cache.
@@ -252,7 +252,10 @@ constexpr int waves_per_simd(int D, bool mx8, bool split, int ht) { return !spli
 // SPLIT: workgroups take shares of the grains and join what they cut; else one takes a whole unit, and the code
 // of shares and joins, whose instructions would be waited for, is left out (4 x 12 rows of 30 keys: 5.6 us, 6.4
 // with it; eight waves for a unit were slower than four: 8 x 500 keys 11.1 us against 10.0).
-template <int D, typename T, bool MX8, bool PAGED16, bool SPLIT, int HT>
+// SHARED: rows begin with positions whose results another kernel has left. (A switch at run time cost calls without them: shares of D = 64
+// kept 7 to 9 registers in scratch memory, and 64 ragged rows of up to 2000 keys of 8 x 64 fp16 took 38.9 us for 36.0, 32 of up to 8000 of 2 x 64 E4M3
+// for 20 heads each 27.6 for 24.1.)
+template <int D, typename T, bool MX8, bool PAGED16, bool SPLIT, int HT, bool SHARED>
 __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void decode_kernel(Args) {
   typedef typename Vec<T>::x8 x8;
   constexpr float kShift = Vec<T>::kShift;
@@ -620,7 +623,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
 
     // On its way during the merge: where the results of the positions that the row shares are.
     i32x4 shared_at = {0, 0, 0, 0};
-    if (fresh(args)->prefix.partial) shared_at = fresh(args)->prefix.rows[b];
+    if constexpr (SHARED) shared_at = fresh(args)->prefix.rows[b];
 
     // Merge the waves, referred to their common maximum: half of them put their rows into LDS, the others add
     // theirs, and the readers below add the remaining ones.
@@ -677,7 +680,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, MX8, SPLIT, HT)) void d
     };
     // The head's results of the positions that its row shares, kDeep splits of them at a time.
     const auto add_shared = [&](int h, int d, f32x4& o, float& top, float& sum) {
-      if (!shared_at[3]) return;
+      if (!SHARED || !shared_at[3]) return;
       const int head = shared_at[2] + kHeads * ht + h;
       const int2 unit = z.prefix.units[shared_at[0] + hk * shared_at[1] + head / kPrefixUnit];
       const int splits = unit.y;
@@ -919,27 +922,33 @@ bool sizes_ok(const mxkv_cache* c, int seqs, int q_heads, int max_len, int windo
          max_len < 1 << 30 && window >= 0 && (int64_t)seqs * q_heads < (int64_t)1 << 24;
 }
 
-template <int D, typename T, bool MX8, bool SPLIT, int HT>
+template <int D, typename T, bool MX8, bool SPLIT, int HT, bool SHARED>
 void launch(const Args& a, unsigned wgs, hipStream_t st) {
   const size_t lds = lds_bytes(D, HT, a.group < 16 * HT ? a.group : 16 * HT, SPLIT);
-  if (a.page_size % 16 == 0) hipLaunchKernelGGL((decode_kernel<D, T, MX8, true, SPLIT, HT>), dim3(wgs), dim3(kThreads), lds, st, a);
-  else hipLaunchKernelGGL((decode_kernel<D, T, MX8, false, SPLIT, HT>), dim3(wgs), dim3(kThreads), lds, st, a);
+  if (a.page_size % 16 == 0) hipLaunchKernelGGL((decode_kernel<D, T, MX8, true, SPLIT, HT, SHARED>), dim3(wgs), dim3(kThreads), lds, st, a);
+  else hipLaunchKernelGGL((decode_kernel<D, T, MX8, false, SPLIT, HT, SHARED>), dim3(wgs), dim3(kThreads), lds, st, a);
 }
 
-template <int D, typename T, bool MX8, int HT>
+template <int D, typename T, bool MX8, int HT, bool SHARED>
 void launch_split(const Args& a, const Plan& p, bool split, hipStream_t st) {
-  if (split) launch<D, T, MX8, true, HT>(a, (unsigned)p.wgs, st);
-  else launch<D, T, MX8, false, HT>(a, (unsigned)p.units, st);
+  if (split) launch<D, T, MX8, true, HT, SHARED>(a, (unsigned)p.wgs, st);
+  else launch<D, T, MX8, false, HT, SHARED>(a, (unsigned)p.units, st);
+}
+
+template <typename T, bool MX8, bool SHARED>
+void launch_dim(const Args& a, const Plan& p, bool split, hipStream_t st) {
+  const int D = padded(a.dim);
+  if (D == 64 && p.ht == 1) launch_split<64, T, MX8, 1, SHARED>(a, p, split, st);
+  else if (D == 64) launch_split<64, T, MX8, 2, SHARED>(a, p, split, st);
+  else if (D == 128 && p.ht == 1) launch_split<128, T, MX8, 1, SHARED>(a, p, split, st);
+  else if (D == 128) launch_split<128, T, MX8, 2, SHARED>(a, p, split, st);
+  else launch_split<256, T, MX8, 1, SHARED>(a, p, split, st);
 }
 
 template <typename T, bool MX8>
-void launch_dim(const Args& a, const Plan& p, bool split, hipStream_t st) {
-  const int D = padded(a.dim);
-  if (D == 64 && p.ht == 1) launch_split<64, T, MX8, 1>(a, p, split, st);
-  else if (D == 64) launch_split<64, T, MX8, 2>(a, p, split, st);
-  else if (D == 128 && p.ht == 1) launch_split<128, T, MX8, 1>(a, p, split, st);
-  else if (D == 128) launch_split<128, T, MX8, 2>(a, p, split, st);
-  else launch_split<256, T, MX8, 1>(a, p, split, st);
+void launch_shared(const Args& a, const Plan& p, bool split, hipStream_t st) {
+  if (a.prefix.partial) launch_dim<T, MX8, true>(a, p, split, st);
+  else launch_dim<T, MX8, false>(a, p, split, st);
 }
 
 }  // namespace
@@ -996,10 +1005,10 @@ int decode_launch(const mxkv_cache* cache, int f, const mx_heads* q, const mx_he
   a.tiles_div = FastDiv((uint32_t)p.tiles);
   a.wgs_div = FastDiv((uint32_t)(split ? p.wgs : 1));
   a.quads_div = FastDiv((uint32_t)cache->dim / 4);
-  if (f == MX_F16 && mx8) launch_dim<_Float16, true>(a, p, split, st);
-  else if (f == MX_F16) launch_dim<_Float16, false>(a, p, split, st);
-  else if (mx8) launch_dim<__bf16, true>(a, p, split, st);
-  else launch_dim<__bf16, false>(a, p, split, st);
+  if (f == MX_F16 && mx8) launch_shared<_Float16, true>(a, p, split, st);
+  else if (f == MX_F16) launch_shared<_Float16, false>(a, p, split, st);
+  else if (mx8) launch_shared<__bf16, true>(a, p, split, st);
+  else launch_shared<__bf16, false>(a, p, split, st);
   return launch_status();
 }
 
