@@ -8,6 +8,7 @@
 // bounds long calls: those 118 MB are at 5.8 TB/s; one row of 4096 takes 4.3 us, most of it the launch. A thread takes units of eight
 // neighbouring elements (16 bytes of 16-bit ones); four lanes hold a block of 32.
 #include <algorithm>
+#include <type_traits>
 
 #include "kvcache.h"
 #include "quant_rules.h"
@@ -57,7 +58,7 @@ MX_DEV uint32_t wave_all(uint32_t x, F f) {
 MX_DEV uint32_t add_bits(uint32_t a, uint32_t b) { return fbits(bitsf(a) + bitsf(b)); }
 MX_DEV uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }  // of magnitudes: NaN above infinity above all
 MX_DEV uint32_t magnitude(float x) { return fbits(x) & 0x7FFFFFFFu; }
-constexpr uint32_t kInf = 0x7F800000u;
+constexpr uint32_t kInf = 0x7F800000u, kFew = 27u << 23, kSmall = 47u << 23;  // infinity, 2^-100, 2^-80
 MX_DEV uint32_t quad_max(uint32_t x) {  // over four neighbouring lanes
   x = max_bits(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false));  // quad_perm: 1 away, 2 away
   return max_bits(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false));
@@ -174,13 +175,16 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
     for (int u = 0; u < U; u++) count(wide(held[u]), c + t + u * kLanes);
   }
   constexpr bool kBlocks = OUT == MX_E4M3 || OUT == MX_E5M2;
-  float factor = 1.f, low = 0.f, pre = 1.f, pre2 = 1.f;  // y = (h pre pre2 w) (factor + low), low: what the factor's rounding leaves, for blocks
+  // y = h pre pre2 before w factor, where one of `before` and `factor` is the row's: a product with the weight alone could leave fp32's
+  // range where y does not. (low: what the factor's rounding leaves, and exact: the factor in 64 bits, both for blocks.)
+  float before = 1.f, factor = 1.f, low = 0.f, pre = 1.f, pre2 = 1.f;
+  double exact = 1.0;
   if (a.norm || OUT == MX_INT8) reduce(sum, top);
   if (a.norm) {
     float eps = a.eps;
-    // Where squares leave fp32's range (sums that overflow, means under 2^-100 that lose bits), or a product with the weight does, the row is
-    // scaled by a power of two that brings its largest element, or the root of eps, to 1. A row with infinities or NaN stays.
-    if (!(sum * a.inv_dim + eps >= 0x1p-100f && sum < INFINITY) || (OUT == MX_INT8 && top >= kInf)) {
+    // Where squares leave fp32's range (sums that overflow, means under 2^-100 that lose bits), the row is scaled by a power of two that brings
+    // its largest element, or the root of eps, to 1. A row with infinities or NaN stays.
+    if (!(sum * a.inv_dim + eps >= 0x1p-100f && sum < INFINITY)) {
       uint32_t most = 0u;
       float none = 0.f;
       each([&](int, x8 v) {
@@ -204,20 +208,33 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
       }
     }
     factor = __builtin_amdgcn_rsqf(fmaf(sum, a.inv_dim, eps));
+    exact = (double)factor;
     if (kBlocks && factor > 0.f && factor < INFINITY) {
       // A block's scale jumps where its largest element passes a power of two, so that element counts to its last bit: one step of Newton's
       // in 64 bits from the approximation.
       const double f = (double)factor, v = whole_sum * a.inv + (double)eps, r = f * (1.5 - 0.5 * v * f * f);
-      factor = (float)r, low = (float)(r - (double)factor);
+      factor = (float)r, low = (float)(r - (double)factor), exact = r;
     }
+    if constexpr (!kBlocks && OUT != MX_INT8) before = factor, factor = 1.f;
   }
 
   const auto g_of = [&](x8 v, int i) -> f32x8 {
     f32x8 h = wide(v);
     if (pre != 1.f || pre2 != 1.f) h = h * pre * pre2;
-    return weighted(h, i);
+    return weighted(h * before, i);
   };
   if constexpr (OUT == MX_INT8) {
+    if (a.norm && !(top >= kFew && top < kInf) && factor < INFINITY) {  // products that leave fp32's range, or vanish in it
+      before = factor, factor = 1.f, top = 0u;
+      float none = 0.f;
+      each([&](int i, x8 v) {
+        const f32x8 y = g_of(v, i);
+#pragma unroll
+        for (int e = 0; e < 8; e++) top = max_bits(top, magnitude(y[e]));
+      });
+      if constexpr (W > 1) __syncthreads();
+      reduce(none, top);
+    }
     const bool fine = top < kInf && factor < INFINITY;
     // small rows are lifted, as 127 / max |g| would overflow
     const float lift = bitsf(top) < 0x1p-60f ? 0x1p64f : 1.f;
@@ -258,11 +275,31 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
 #pragma unroll
       for (int e = 0; e < 8; e++) y[e] = fmaf(g[e], factor, rest[e]), amax = max_bits(amax, magnitude(y[e]));
       amax = quad_max(amax);
+      // Where g left fp32's range, or vanished in it and the factor (at most 2^50) makes it larger again: in 64 bits. (binary16's cannot.)
+      bool far = false;
+      if constexpr (!std::is_same_v<T, _Float16>) {
+        far = a.norm && (amax >= kInf || (amax < kSmall && factor > 1.f));
+        if (__any(far)) {
+          const f32x8 h = wide(v);
+          f32x8 w;
+#pragma unroll
+          for (int e = 0; e < 8; e++) w[e] = 1.f;
+          if (weight) w = wide(load(weight, i));
+          uint32_t most = 0u;
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const double d = (double)h[e] * pre * pre2 * w[e] * exact;
+            if (far) y[e] = (float)d, rest[e] = (float)(d - (double)y[e]);
+            most = max_bits(most, magnitude(y[e]));
+          }
+          amax = quad_max(most);
+        }
+      }
       if (__any((amax & 0x7FFFFFu) == 0u && amax > 0u && amax < kInf)) {  // a power of two, or what was rounded up to it
         uint32_t below = 0u;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          const float left = fmaf(g[e], factor, -y[e]) + rest[e];  // of y's rounding
+          const float left = far ? rest[e] : fmaf(g[e], factor, -y[e]) + rest[e];  // of y's rounding
           below = max_bits(below, magnitude(y[e]) - ((left < 0.f && y[e] > 0.f) || (left > 0.f && y[e] < 0.f) ? 1u : 0u));
         }
         below = quad_max(below);

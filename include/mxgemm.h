@@ -308,7 +308,8 @@ typedef struct {
  *    or NaN scale NaN and zeros. MX_E4M3 and MX_E5M2 (dim % 32 == 0): the codes and E8M0 scales, [rows][dim / 32], that mx_pack_run's rule
  *    gives y, the scale that of y before its rounding to fp32, for mxgemm_run (which wants out->stride == dim).
  *  - Squares are summed and y is formed in fp32, and rounded once. Rows whose squares pass fp32's range (or vanish in it) are
- *    scaled by a power of two first, so every finite row has its norm.
+ *    scaled by a power of two first, and a product with the weight that does is formed otherwise, so every finite row has its norm, whatever
+ *    finite weights it has. (A row of zeros with eps 0 has none: its y is NaN.)
  * 1 <= dim <= MX_MAX_DIM, 0 <= rows <= MX_MAX_DIM (0: nothing is done); strides at least dim, in multiples of 16 bytes; eps finite and
  * not negative. Besides total, outputs must not overlap inputs. Elements between dim and the stride are neither
  * read nor written.
