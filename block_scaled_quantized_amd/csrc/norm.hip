@@ -4,8 +4,8 @@
 // h = round(x + r),  y_i = h_i w_i / sqrt(mean h^2 + eps). With g_i = h_i w_i the row's factor is left out of what needs a whole row: the
 // sum of squares and the largest |g| are one pass and one reduction, 8-bit integers are q = rint(g 127 / max |g|), whose scale alone
 // has the factor, and the others are g times the factor. So a row is read once, held in registers as it was rounded, and
-// written once, what is as wide as the input by non-temporal stores (4096 x 4096, bf16 with residual to E4M3: 20.2 us, with plain ones 25.4). Memory
-// bounds long calls: those 118 MB are at 5.8 TB/s; one row of 4096 takes 4.3 us, most of it the launch. A thread takes units of eight
+// written once, what is as wide as the input by non-temporal stores (4096 x 4096, bf16 with residual to E4M3: 20.4 us, with plain ones 25.4). Memory
+// bounds long calls: those 118 MB are at 5.8 TB/s; one row of 4096 takes 4.3 to 4.9 us, most of it the launch. A thread takes units of eight
 // neighbouring elements (16 bytes of 16-bit ones); four lanes hold a block of 32.
 #include <algorithm>
 #include <type_traits>
@@ -38,7 +38,7 @@ struct Args {
   void *total, *out, *scales;
   int64_t x_stride, residual_stride, total_stride, out_stride;  // elements
   int rows, dim;
-  float eps, inv_dim;
+  float eps;
   double inv;  // 1 / dim
   int norm;
 };
@@ -56,8 +56,31 @@ MX_DEV uint32_t wave_all(uint32_t x, F f) {
   return f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xF, 0xF, false));
 }
 MX_DEV uint32_t add_bits(uint32_t a, uint32_t b) { return fbits(bitsf(a) + bitsf(b)); }
+MX_DEV float wave_sum(float x) { return bitsf(wave_all(fbits(x), add_bits)); }
+// The same in 64 bits, whose halves are exchanged each.
+MX_DEV double wave_sum(double x) {
+  const auto halves = [](double v) { return __builtin_bit_cast(u32x2, v); };
+  const auto whole = [](uint32_t lo, uint32_t hi) { return __builtin_bit_cast(double, (u32x2){lo, hi}); };
+  const auto swapped = [&](auto swap) {
+    const u32x2 w = halves(x);
+    const auto lo = swap(w[0]), hi = swap(w[1]);
+    x = whole(lo[0], hi[0]) + whole(lo[1], hi[1]);
+  };
+  swapped([](uint32_t w) { return __builtin_amdgcn_permlane32_swap(w, w, false, false); });
+  swapped([](uint32_t w) { return __builtin_amdgcn_permlane16_swap(w, w, false, false); });
+  const auto turned = [&](auto turn) {
+    const u32x2 w = halves(x);
+    x += whole(turn(w[0]), turn(w[1]));
+  };
+  turned([](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x128, 0xF, 0xF, false); });
+  turned([](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x124, 0xF, 0xF, false); });
+  turned([](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x122, 0xF, 0xF, false); });
+  turned([](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x121, 0xF, 0xF, false); });
+  return x;
+}
 MX_DEV uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }  // of magnitudes: NaN above infinity above all
 MX_DEV uint32_t magnitude(float x) { return fbits(x) & 0x7FFFFFFFu; }
+constexpr double kNear = 0x1p-40;  // an element this near below a power of two counts as it: the row's factor in 64 bits is good for so much
 constexpr uint32_t kInf = 0x7F800000u, kFew = 27u << 23, kSmall = 47u << 23;  // infinity, 2^-100, 2^-80
 MX_DEV uint32_t quad_max(uint32_t x) {  // over four neighbouring lanes
   x = max_bits(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false));  // quad_perm: 1 away, 2 away
@@ -75,7 +98,12 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
   typedef typename Eight<T>::type x8;
   typedef x8 stored __attribute__((aligned(16)));  // rows are 16-byte aligned
   constexpr int kLanes = 64 * W, kChunk = kLanes * U;
-  __shared__ uint32_t wave_sum[W], wave_top[W];
+  // A block's scale jumps where its largest element passes a power of two, so that element counts to its last bits, and so do the row's sum and
+  // factor: in 64 bits for blocks (4096 x 4096: 20.4 us; 19.9 with a sum in 32, which gave most rows of one size the wrong scale).
+  constexpr bool kBlocks = OUT == MX_E4M3 || OUT == MX_E5M2;
+  typedef std::conditional_t<kBlocks, double, float> Sum;
+  __shared__ Sum sums[W];
+  __shared__ uint32_t tops[W];
   const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, wave = threadIdx.x >> 6;
   const int row = W == 1 ? (int)blockIdx.x * kRowsOfWaves + __builtin_amdgcn_readfirstlane(wave) : (int)blockIdx.x;
   if (W == 1 && row >= a.rows) return;
@@ -130,29 +158,25 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
       }
     }
   };
-  // the row's sum of squares and largest magnitude, from the threads' own (the waves' sums are added in 64 bits)
-  double whole_sum = 0.0;
-  const auto reduce = [&](float& sum, uint32_t& top) {
-    uint32_t s = wave_all(fbits(sum), add_bits);
+  // the row's sum of squares and largest magnitude, from the threads' own
+  const auto reduce = [&](Sum& sum, uint32_t& top) {
+    sum = wave_sum(sum);
     top = wave_all(top, max_bits);
     if constexpr (W > 1) {
-      if ((threadIdx.x & 63) == 0) wave_sum[wave] = s, wave_top[wave] = top;
+      if ((threadIdx.x & 63) == 0) sums[wave] = sum, tops[wave] = top;
       __syncthreads();
-      whole_sum = (double)bitsf(wave_sum[0]), top = wave_top[0];
+      sum = sums[0], top = tops[0];
 #pragma unroll
-      for (int w = 1; w < W; w++) whole_sum += (double)bitsf(wave_sum[w]), top = max_bits(top, wave_top[w]);
-      sum = (float)whole_sum;
-    } else {
-      sum = bitsf(s), whole_sum = (double)sum;
+      for (int w = 1; w < W; w++) sum += sums[w], top = max_bits(top, tops[w]);
     }
   };
 
-  float sum = 0.f;
+  Sum sum = 0;
   uint32_t top = 0u;  // of |g|
   const auto count = [&](f32x8 h, int i) {
     const f32x8 g = weighted(h, i);
 #pragma unroll
-    for (int e = 0; e < 8; e++) sum = fmaf(h[e], h[e], sum);
+    for (int e = 0; e < 8; e++) sum = __builtin_elementwise_fma((Sum)h[e], (Sum)h[e], sum);
     if constexpr (OUT == MX_INT8) {
 #pragma unroll
       for (int e = 0; e < 8; e++) top = max_bits(top, magnitude(g[e]));
@@ -174,19 +198,19 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
 #pragma unroll
     for (int u = 0; u < U; u++) count(wide(held[u]), c + t + u * kLanes);
   }
-  constexpr bool kBlocks = OUT == MX_E4M3 || OUT == MX_E5M2;
   // y = h pre pre2 before w factor, where one of `before` and `factor` is the row's: a product with the weight alone could leave fp32's
-  // range where y does not. (low: what the factor's rounding leaves, and exact: the factor in 64 bits, both for blocks.)
-  float before = 1.f, factor = 1.f, low = 0.f, pre = 1.f, pre2 = 1.f;
+  // range where y does not. (exact: the factor in 64 bits, for blocks.)
+  float before = 1.f, factor = 1.f, pre = 1.f, pre2 = 1.f;
   double exact = 1.0;
   if (a.norm || OUT == MX_INT8) reduce(sum, top);
   if (a.norm) {
     float eps = a.eps;
+    const auto mean = [&] { return (float)(sum * (Sum)a.inv + (Sum)eps); };
     // Where squares leave fp32's range (sums that overflow, means under 2^-100 that lose bits), the row is scaled by a power of two that brings
     // its largest element, or the root of eps, to 1. A row with infinities or NaN stays.
-    if (!(sum * a.inv_dim + eps >= 0x1p-100f && sum < INFINITY)) {
+    if (!(mean() >= 0x1p-100f && mean() < INFINITY)) {
       uint32_t most = 0u;
-      float none = 0.f;
+      Sum none = 0;
       each([&](int, x8 v) {
         const f32x8 h = wide(v);
 #pragma unroll
@@ -199,7 +223,7 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
         const int half = -e / 2, rest = -e - half;
         pre = pow2(half), pre2 = pow2(rest);
         eps = eps * pre * pre2 * pre * pre2;
-        sum = 0.f, top = 0u;
+        sum = 0, top = 0u;
         each([&](int i, x8 v) { count(wide(v) * pre * pre2, i); });
         if constexpr (W > 1) __syncthreads();
         reduce(sum, top);
@@ -207,13 +231,12 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
         eps = 1.f;  // zeros, whatever the root of a subnormal is
       }
     }
-    factor = __builtin_amdgcn_rsqf(fmaf(sum, a.inv_dim, eps));
+    factor = __builtin_amdgcn_rsqf(mean());
     exact = (double)factor;
     if (kBlocks && factor > 0.f && factor < INFINITY) {
-      // A block's scale jumps where its largest element passes a power of two, so that element counts to its last bit: one step of Newton's
-      // in 64 bits from the approximation.
-      const double f = (double)factor, v = whole_sum * a.inv + (double)eps, r = f * (1.5 - 0.5 * v * f * f);
-      factor = (float)r, low = (float)(r - (double)factor), exact = r;
+      // one step of Newton's from the approximation, whose error of 2^-23 becomes 2^-45
+      const double f = (double)factor, v = sum * a.inv + (double)eps, r = f * (1.5 - 0.5 * v * f * f);
+      factor = (float)r, exact = r;
     }
     if constexpr (!kBlocks && OUT != MX_INT8) before = factor, factor = 1.f;
   }
@@ -226,7 +249,7 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
   if constexpr (OUT == MX_INT8) {
     if (a.norm && !(top >= kFew && top < kInf) && factor < INFINITY) {  // products that leave fp32's range, or vanish in it
       before = factor, factor = 1.f, top = 0u;
-      float none = 0.f;
+      Sum none = 0;
       each([&](int i, x8 v) {
         const f32x8 y = g_of(v, i);
 #pragma unroll
@@ -260,50 +283,32 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
     uint8_t* out = (uint8_t*)a.out + row * a.out_stride;
     uint8_t* scales = (uint8_t*)a.scales + (int64_t)row * (dim / 32);
     each([&](int i, x8 v) {
-      const f32x8 g = g_of(v, i);
-      f32x8 y, rest = g * low;
-      if constexpr (sizeof(T) == 4) {  // 16-bit elements' products with the weights are exact
-        if (weight) {
-          f32x8 h = wide(v);
-          if (pre != 1.f || pre2 != 1.f) h = h * pre * pre2;
-          const f32x8 w = wide(load(weight, i));
-#pragma unroll
-          for (int e = 0; e < 8; e++) rest[e] = fmaf(fmaf(h[e], w[e], -g[e]), factor, rest[e]);
-        }
-      }
+      f32x8 y = g_of(v, i) * factor;
       uint32_t amax = 0u;
 #pragma unroll
-      for (int e = 0; e < 8; e++) y[e] = fmaf(g[e], factor, rest[e]), amax = max_bits(amax, magnitude(y[e]));
+      for (int e = 0; e < 8; e++) amax = max_bits(amax, magnitude(y[e]));
       amax = quad_max(amax);
-      // Where g left fp32's range, or vanished in it and the factor (at most 2^50) makes it larger again: in 64 bits. (binary16's cannot.)
-      bool far = false;
-      if constexpr (!std::is_same_v<T, _Float16>) {
-        far = a.norm && (amax >= kInf || (amax < kSmall && factor > 1.f));
-        if (__any(far)) {
-          const f32x8 h = wide(v);
-          f32x8 w;
+      // In 64 bits: next to a power of two (y is off by three half steps at most), and where the product with the weight left fp32's range, or
+      // vanished in it and the factor (at most 2^50) makes it larger again (binary16's cannot).
+      bool closer = ((amax + 4u) & 0x7FFFFFu) < 8u && amax > 0u;
+      if constexpr (!std::is_same_v<T, _Float16>) closer |= amax >= kInf || (amax < kSmall && factor > 1.f);
+      if (a.norm && __any(closer)) {
+        x8 anew = v;
+        asm("" : "+v"(anew));  // here, and not kept in 64 bits since the sum
+        const f32x8 h = wide(anew);
+        f32x8 w;
 #pragma unroll
-          for (int e = 0; e < 8; e++) w[e] = 1.f;
-          if (weight) w = wide(load(weight, i));
-          uint32_t most = 0u;
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const double d = (double)h[e] * pre * pre2 * w[e] * exact;
-            if (far) y[e] = (float)d, rest[e] = (float)(d - (double)y[e]);
-            most = max_bits(most, magnitude(y[e]));
-          }
-          amax = quad_max(most);
-        }
-      }
-      if (__any((amax & 0x7FFFFFu) == 0u && amax > 0u && amax < kInf)) {  // a power of two, or what was rounded up to it
-        uint32_t below = 0u;
+        for (int e = 0; e < 8; e++) w[e] = 1.f;
+        if (weight) w = wide(load(weight, i));
+        uint32_t most = 0u;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          const float left = far ? rest[e] : fmaf(g[e], factor, -y[e]) + rest[e];  // of y's rounding
-          below = max_bits(below, magnitude(y[e]) - ((left < 0.f && y[e] > 0.f) || (left > 0.f && y[e] < 0.f) ? 1u : 0u));
+          const double d = (double)h[e] * pre * pre2 * w[e] * exact;
+          if (closer) y[e] = (float)d;
+          // what was rounded up to a power of two has the scale of what is below
+          most = max_bits(most, magnitude(y[e]) - (fabs(d) < (1.0 - kNear) * fabs((double)y[e]) ? 1u : 0u));
         }
-        below = quad_max(below);
-        if (amax < kInf) amax = below;
+        amax = closer ? quad_max(most) : amax;
       }
       int shift;
       const uint32_t E = mx_block_scale(amax, amax >= kInf, OUT, &shift);
@@ -350,7 +355,7 @@ void launch(const Args& a, hipStream_t st) {
 
 // Short rows: a wave to each, which needs no barrier. Longer ones: as many waves as make a row's chain of latencies short and still let rows
 // follow one another on a CU, so that some load while others store. With many rows a thread has two units on their way (4096
-// x 4096, bf16 with residual to E4M3: 20.2 us of four waves, 26 of eight, 28 of one; 512 rows: 4.7 and 4.5 of eight).
+// x 4096, bf16 with residual to E4M3: 20.4 us of four waves, 26 of eight, 28 of one; 512 rows: 4.7 and 4.5 of eight).
 template <typename T, int OUT>
 void launch_shape(const Args& a, hipStream_t st) {
   const int units = ceil_div(a.dim, 8);
@@ -398,7 +403,7 @@ int run(Args a, int f, int rows, int dim, const mx_rows* x, const mx_rows* resid
   if (residual) a.residual = residual->data, a.residual_stride = residual->stride;
   if (total) a.total = total->data, a.total_stride = total->stride;
   a.out = out->data, a.out_stride = out->stride, a.scales = scales;
-  a.inv = 1.0 / dim, a.inv_dim = (float)a.inv;
+  a.inv = 1.0 / dim;
   if (int s = check_arch()) return s;
   const hipStream_t st = as_stream(stream);
   if (f == MX_F16) launch_out<_Float16, MX_F16>(a, fmt, st);

@@ -306,7 +306,8 @@ typedef struct {
  *  - fmt: what y is written as. f: y rounded, scales unused. MX_INT8: out bytes q = rint(127 y / max|y|) of the row, ties to
  *    even, and scales, fp32 [rows], max|y| / 127, for mxgemm_i8_run; a row of zeros has scale 0, a row with an infinity
  *    or NaN scale NaN and zeros. MX_E4M3 and MX_E5M2 (dim % 32 == 0): the codes and E8M0 scales, [rows][dim / 32], that mx_pack_run's rule
- *    gives y, the scale that of y before its rounding to fp32, for mxgemm_run (which wants out->stride == dim).
+ *    gives y, the scale that of y before its rounding to fp32 (within 2^-40 below a power of two, y counts as that power), for mxgemm_run
+ *    (which wants out->stride == dim).
  *  - Squares are summed and y is formed in fp32, and rounded once. Rows whose squares pass fp32's range (or vanish in it) are
  *    scaled by a power of two first, and a product with the weight that does is formed otherwise, so every finite row has its norm, whatever
  *    finite weights it has. (A row of zeros with eps 0 has none: its y is NaN.)
