@@ -200,8 +200,10 @@ MX_DEV void barrier() {
 template <int D, typename T, bool MX8, bool CAP>
 __global__ __launch_bounds__(threads_of(D), halves_of(D)) void prefix_kernel(Args a) {
   typedef typename Vec<T>::x8 x8;
-  // A probability is at most 2^kSlack. binary16's are scaled by as much less, so that they stay in its range.
-  constexpr float kSlack = 6.f, kShift = Vec<T>::kShift > 0.f ? Vec<T>::kShift - kSlack : 0.f;
+  // A probability is at most 2^kSlack. binary16's, scaled by 2^15, stay in its range below 2: scaled by 2^9, for the same 2^6, the least second part would be
+  // 2^-33 of the largest, which runs of thousands of keys that count nothing beside one would show (3 times the decode call's bound; 96 rows in five
+  // groups E4M3: 130 us, and 132 as it is, with more turns that rescale).
+  constexpr float kShift = Vec<T>::kShift, kSlack = kShift > 0.f ? 0.99f : 6.f;
   constexpr int kThreads = threads_of(D), kHalves = halves_of(D), kWaves = kThreads / 64, kKeys = keys_of(D);
   constexpr int kSteps = D / 16, kOut = D / 32;
   constexpr int kPitch = 2 * D, kPlane = kKeys * kPitch;                     // bytes of a key's row in LDS, and of a tile
@@ -561,7 +563,6 @@ __global__ __launch_bounds__(threads_of(D), halves_of(D)) void prefix_kernel(Arg
     {
       const auto r = __builtin_amdgcn_permlane32_swap(fbits(l), fbits(l), false, false);
       l = bitsf(r[0]) + bitsf(r[1]);
-      m += Vec<T>::kShift - kShift;  // the decode kernel's sums are scaled by its own shift
       const int lane = anew(threadIdx.x) & 63, c = lane & 31, h = lane >> 5, width = anew(dim);
       f32x4* const shared_acc = reinterpret_cast<f32x4*>(lds) + row_wave * 8 * D + h * 32 + c;  // [D / 4][32]
       if constexpr (kHalves == 2) {

@@ -500,7 +500,7 @@ typedef struct {
  *    its own table row. A group with one row that has positions shares nothing.
  *  - There is no window (opts->window: 0) and there are no starts. Other rules, and the treatment of missing pages, empty rows and lse, are
  *    mxattn_decode_run's; 0 <= count <= 1024, max_shared >= 0 (MX_ERR_SHAPE).
- *  - Results are the same up to fp32 summation order.
+ *  - Results are the same up to fp32 summation order and the probabilities' rounding, which hold 21 bits in binary16 and 15 in bfloat16 in both calls.
  * Workspace as for mxattn_decode_run, of mxattn_prefix_workspace_size() bytes (the buffers of the two are interchangeable where large enough). Without
  * one, or with too small a one, nothing is shared: every row is read by itself. So it is where max_len, max_shared and the numbers of rows and groups leave less
  * than some 64 MB that need not be read again, as a pass of its own would take longer; the results are those of mxattn_decode_run then.
