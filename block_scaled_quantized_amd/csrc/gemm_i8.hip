@@ -424,9 +424,12 @@ Plan plan_for(int M, int N, int K, bool can_split) {
     return p;
   }
   // The largest tiles that fill three quarters of the CUs (1024 x 14336 x 4096: 256 wide 60 us, 128 wide 78; 256 x 12288 x 4096: 128 wide 22, 64 wide 32;
-  // 512 x 4096 x 4096: 64 wide 17.5 us, 128 wide and K split 21).
+  // 512 x 4096 x 4096: 64 wide 17.5 us, 128 wide and K split 21), but none that the rows or columns would fill half at most: the time is then that of
+  // the other operand's bytes (1 x 70000 x 4096, and 70000 x 16 x 4096: 64 wide 67 us, 256 wide 123 to 127; 64 x 128256 x 4096: 112 to 118 and 139 to 144;
+  // 128 x 70000 x 4096: 128 wide 103, 256 wide 129, 64 wide 98).
   const auto tiles = [&](int side) { return (int64_t)ceil_div(M, side) * ceil_div(N, side); };
-  p.side = tiles(256) >= kCUs * 3 / 4 ? 256 : tiles(128) >= kCUs * 3 / 4 ? 128 : 64;
+  const int most = std::min(M, N) <= 64 ? 64 : std::min(M, N) <= 128 ? 128 : 256;
+  p.side = most >= 256 && tiles(256) >= kCUs * 3 / 4 ? 256 : most >= 128 && tiles(128) >= kCUs * 3 / 4 ? 128 : 64;
   p.tiles_m = ceil_div(M, p.side), p.tiles_n = ceil_div(N, p.side);
   const int64_t n = tiles(p.side);
   // Small tiles that leave CUs idle split K, four slots at least to a workgroup (64 x 4096 x 4096: 10.6 us in four, 10.5 in two, 13.8 in

@@ -195,3 +195,11 @@ def test_normalised_rows_times_quantised_weights(M):
     err = np.abs(f64(C) - want) / (6 * sigma + 2.0 ** -11 * np.abs(want))
     say(f"chain of {M} rows: worst error / bound {err.max():.3f}")
     assert err.max() <= 1.0
+
+
+@pytest.mark.parametrize("few", [1, 16, 17, 64, 65, 128, 129])
+@pytest.mark.parametrize("many,K", [(24449, 100), (48897, 65), (70001, 160), (128256, 32)])
+def test_few_rows_of_many_columns(few, many, K):
+    """A vocabulary's projection of a few tokens, and as many rows by few columns."""
+    run(few, many, K, "f16", few + many + K, pad=(few % 3, many % 2))
+    run(many, few, K, "bf16", few + many + K, bias=True, relu=True)
