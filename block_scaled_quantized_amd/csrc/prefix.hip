@@ -13,7 +13,7 @@
 // What bounds it: one round of workgroups, each of which works out the shares and fetches its first keys (some 15000 clocks) before turns of 128
 // keys, 6100 to 6700 clocks for 128 rows, in which the matrix cores have 35% and the vector units most of the rest. 64 rows of 64 heads behind 8192
 // positions of 8 x 128 bf16: 38 us here, 36 in the decode kernel (512 positions of each row and the joining of 17 MB of partial results), where
-// the decode kernel alone takes 335. 96 rows in five groups behind up to 12000 positions, E4M3: 80 to 95 us and 52, alone 232.
+// the decode kernel alone takes 335. 96 rows in five groups behind up to 12000 positions, E4M3: 85 to 101 us and 52, alone 232.
 #include <algorithm>
 
 #include "attention.h"
@@ -615,7 +615,9 @@ size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 bool sizes_ok(int groups, int max_shared) { return groups >= 0 && groups <= kMaxGroups && max_shared >= 0; }
 
 // Whether there may be enough to share: a pass of its own and the joining of its results take some 12 us, in which the decode kernel reads 64 MB
-// (4 rows behind 992 positions of 8 x 128 fp16, 12 MB that need not be read again: 11.5 us without, 20 with).
+// (4 rows behind 992 positions of 8 x 128 fp16, 12 MB that need not be read again: 11.5 us without, 20 with). A turn of 128 keys takes as long for few
+// rows as for 128, which is not weighed: 16 groups of 4 rows behind 4096 positions of 8 x 128 take 90 us and 154 without (E4M3: 82 and 82), of 2 rows 80
+// and 75 (E4M3: 82 and 49).
 bool worth(const mxkv_cache* c, int seqs, int groups, int max_len, int max_shared) {
   const int shared = std::min(max_len, max_shared), again = std::max(0, seqs - groups);
   return groups > 0 && shared >= kLeastShared && (double)again * shared * c->heads * c->dim * (c->fmt == MX_E4M3 ? 2 : 4) >= (double)(64 << 20);

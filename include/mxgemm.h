@@ -308,7 +308,7 @@ typedef struct {
  *    or NaN scale NaN and zeros. MX_E4M3 and MX_E5M2 (dim % 32 == 0): the codes and E8M0 scales, [rows][dim / 32], that mx_pack_run's rule
  *    gives y, the scale that of y before its rounding to fp32 (within 2^-40 below a power of two, y counts as that power), for mxgemm_run
  *    (which wants out->stride == dim).
- *  - Squares are summed and y is formed in fp32, and rounded once. Rows whose squares pass fp32's range (or vanish in it) are
+ *  - Squares are summed (for blocks in 64 bits) and y is formed in fp32, and rounded once. Rows whose squares pass fp32's range (or vanish in it) are
  *    scaled by a power of two first, and a product with the weight that does is formed otherwise, so every finite row has its norm, whatever
  *    finite weights it has. (A row of zeros with eps 0 has none: its y is NaN.)
  * 1 <= dim <= MX_MAX_DIM, 0 <= rows <= MX_MAX_DIM (0: nothing is done); strides at least dim, in multiples of 16 bytes; eps finite and
@@ -338,7 +338,8 @@ int mxquant_rows_run(int f, int rows, int dim, const mx_rows* x, int fmt, const 
  * not matter.
  * Workspace as for mxmatvec_run, of mxgemm_i8_workspace_size() bytes, zero-filled before its first use and left reusable by every
  * call, of this or other shapes: where there are few tiles, workgroups split K and their sums meet there. Calls that may overlap in time need separate
- * workspaces. Without one, or with too small a one, K is not split.
+ * workspaces, and so do calls of another kind (mxmatvec_run, attention), which keep their counters at other places. Without one, or with too small a one, K is
+ * not split.
  */
 int mxgemm_i8_run(int M, int N, int K, const mx_rows* A, const float* SA, const mx_rows* B, const float* SB, const void* bias, int fc,
                   const mx_rows* C, unsigned flags, void* workspace, size_t workspace_bytes, void* stream);
@@ -469,7 +470,8 @@ typedef struct {
  * Workspace, as for mxmatvec_run: the rows' keys are shared evenly among workgroups, and where a share
  * cuts a row, partial results and counters live in a caller-owned device buffer of
  * mxattn_decode_workspace_size() bytes, zero-filled before its first use and left reusable by every
- * call, of this or other shapes. Calls that may overlap in time need separate workspaces. Without one, or with too small a one, a
+ * call, of this or other shapes. Calls that may overlap in time need separate workspaces, and so do calls other than attention (mxmatvec_run,
+ * mxgemm_i8_run), which keep their counters at other places. Without one, or with too small a one, a
  * row is not cut (same results up to fp32 summation order; slow for long rows). The
  * partials are joined in a fixed order: results are deterministic.
  * Rules (MX_ERR_SHAPE): q->heads a multiple of the cache's heads, out->heads == q->heads;
@@ -503,7 +505,9 @@ typedef struct {
  *  - Results are the same up to fp32 summation order and the probabilities' rounding, which hold 21 bits in binary16 and 15 in bfloat16 in both calls.
  * Workspace as for mxattn_decode_run, of mxattn_prefix_workspace_size() bytes (the buffers of the two are interchangeable where large enough). Without
  * one, or with too small a one, nothing is shared: every row is read by itself. So it is where max_len, max_shared and the numbers of rows and groups leave less
- * than some 64 MB that need not be read again, as a pass of its own would take longer; the results are those of mxattn_decode_run then.
+ * than some 64 MB that need not be read again, as a pass of its own would take longer; the results are those of mxattn_decode_run then. How few rows a group has
+ * is not weighed: groups of two over a 16-bit cache, and of up to four over E4M3, take up to twice as long as with mxattn_decode_run, and so do short rows
+ * under bounds far above them.
  */
 int mxattn_prefix_run(const mxkv_cache* cache, int f, const mx_heads* q, const mx_heads* out, float* lse, const mxkv_table* table,
                       const int32_t* lengths, const mxattn_groups* groups, int max_len, const mxattn_opts* opts, void* workspace,
@@ -545,7 +549,7 @@ int mxkv_copy_run(const mxkv_cache* layers, int n_layers, const int32_t* pairs, 
  *  - lengths_out = the new lengths and *n_free_out (each may be what it was read from), *status = 0. Where the step is not
  *    possible, *status is a sum of MXKV_STEP_ bits, lengths and n_free are copied, the table and the stack stay, and the step
  *    has no tokens.
- * lengths outside 0 .. cols * page_size are taken as that bound. A row's cells of the positions that it has are expected
+ * lengths outside 0 .. cols * page_size, and n_free outside 0 .. pages, are taken as that bound. A row's cells of the positions that it has are expected
  * to hold its pages, as calls leave them, and the stack to hold free ones.
  * Rules (MX_ERR_SHAPE): 0 <= seqs (0: nothing is done), pages, page_size, max_tokens <= MX_MAX_DIM; cols * page_size and pages * page_size below 2^31.
  */
