@@ -3,10 +3,10 @@
 //
 // h = round(x + r),  y_i = h_i w_i / sqrt(mean h^2 + eps). With g_i = h_i w_i the row's factor is left out of what needs a whole row: the
 // sum of squares and the largest |g| are one pass and one reduction, 8-bit integers are q = rint(g 127 / max |g|), whose scale alone
-// has the factor, and the others are g times the factor, or h times the factor times w where they have the input's own type. So a row is read once, held in registers as it was rounded, and
-// written once, what is as wide as the input by non-temporal stores (4096 x 4096, bf16 with residual to E4M3: 20.4 us, with plain ones 25.4). Memory
-// bounds long calls: those 118 MB are at 5.8 TB/s; one row of 4096 takes 4.3 to 4.9 us, most of it the launch. A thread takes units of eight
-// neighbouring elements (16 bytes of 16-bit ones); four lanes hold a block of 32.
+// has the factor, and the others are g times the factor, or h times the factor times w where they have the input's own type. So a row
+// is read once, held in registers as it was rounded, and written once, what is as wide as the input by non-temporal stores (4096 x 4096, bf16 with
+// residual to E4M3: 20.4 us, with plain ones 25.4). Memory bounds long calls: those 118 MB are at 5.8 TB/s; one row of 4096 takes 4.3 to 4.9 us, most
+// of it the launch. A thread takes units of eight neighbouring elements (16 bytes of 16-bit ones); four lanes hold a block of 32.
 #include <algorithm>
 #include <type_traits>
 
@@ -158,16 +158,18 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
       }
     }
   };
-  // the row's sum of squares and largest magnitude, from the threads' own
+  // the row's sum of squares and largest magnitude, from the threads' own (the waves' sums are added in 64 bits)
   const auto reduce = [&](Sum& sum, uint32_t& top) {
     sum = wave_sum(sum);
     top = wave_all(top, max_bits);
     if constexpr (W > 1) {
       if ((threadIdx.x & 63) == 0) sums[wave] = sum, tops[wave] = top;
       __syncthreads();
-      sum = sums[0], top = tops[0];
+      double all = (double)sums[0];
+      top = tops[0];
 #pragma unroll
-      for (int w = 1; w < W; w++) sum += sums[w], top = max_bits(top, tops[w]);
+      for (int w = 1; w < W; w++) all += (double)sums[w], top = max_bits(top, tops[w]);
+      sum = (Sum)all;
     }
   };
 
@@ -292,7 +294,7 @@ __global__ __launch_bounds__(W == 1 ? 64 * kRowsOfWaves : 64 * W) void norm_kern
       // vanished in it and the factor (at most 2^50) makes it larger again (binary16's cannot).
       bool closer = ((amax + 4u) & 0x7FFFFFu) < 8u && amax > 0u;
       if constexpr (!std::is_same_v<T, _Float16>) closer |= amax >= kInf || (amax < kSmall && factor > 1.f);
-      if (a.norm && __any(closer)) {
+      if (a.norm && sum != 0 && __any(closer)) {  // (a row of zeros has none)
         x8 anew = v;
         asm("" : "+v"(anew));  // here, and not kept in 64 bits since the sum
         const f32x8 h = wide(anew);
