@@ -62,3 +62,15 @@ def test_weights_take_elements_to_powers_of_two(kind, dim):
     want = np.floor(np.log2(w.reshape(-1, 32).max(1))).astype(int) - 8 + 127
     got = host(scales).astype(int)
     assert np.array_equal(got, np.broadcast_to(want, got.shape)), (got != want).any(1).sum()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_longest_rows(kind):
+    """Rows of 2^20 elements, whose sums lose the most: exactly 1, and below it by 2^-38 and more."""
+    api = require_gpu()
+    dim, c = 1 << 20, constants(kind, 9)[:4]
+    x = torch.from_numpy(np.repeat(c[:, None], dim, 1)).to(TORCH[kind]).cuda()
+    codes, scales = torch.zeros(4, dim, dtype=torch.uint8, device="cuda"), torch.zeros(4, dim // 32, dtype=torch.uint8, device="cuda")
+    for eps, below in ((0.0, 0), (2.0 ** -35, 1)):
+        api.mxnorm_run(fmt_of(api, kind), x, codes, scales, api.MX_E4M3, eps=eps)
+        assert bool((scales == 119 - below).all()), eps
